@@ -68,6 +68,12 @@ fa_status device_setup(DeviceInfo** out) {
   return FA_OK;
 }
 
+#define FA_TRY(expr)                   \
+  do {                                 \
+    const fa_status st_ = (expr);      \
+    if (st_ != FA_OK) return st_;      \
+  } while (0)
+
 int64_t elem_size(fa_dtype dt) { return dt == FA_F32 ? 4 : 2; }
 
 bool mul_ok(int64_t a, int64_t b, int64_t* r) { return !__builtin_mul_overflow(a, b, r); }
@@ -109,15 +115,21 @@ fa_status check_f32_vec(const void* p) {
   return FA_OK;
 }
 
+// check_tensor for the entry points that also refuse a stride of 0 (a
+// broadcast dimension): a tensor map cannot carry one, and rows of an output
+// would fall on one another.
+fa_status check_dense(const void* p, const int64_t* s, int64_t B, int64_t H, int64_t N,
+                      fa_dtype dt, int64_t* dst) {
+  FA_TRY(check_tensor(p, s, B, H, N, dt, dst));
+  const int64_t ext[3] = {B, H, N};
+  for (int i = 0; i < 3; ++i)
+    if (ext[i] > 1 && s[i] == 0) return FA_ERR_STRIDE;
+  return FA_OK;
+}
+
 fa_status check_scale(float scale) {
   return (std::isfinite(scale) && scale > 0.f) ? FA_OK : FA_ERR_SCALE;
 }
-
-#define FA_TRY(expr)                   \
-  do {                                 \
-    const fa_status st_ = (expr);      \
-    if (st_ != FA_OK) return st_;      \
-  } while (0)
 
 bool use_tc(fa_dtype dt) { return g_path.load() == FA_PATH_AUTO && dt != FA_F32; }
 
@@ -505,6 +517,172 @@ fa_status fa_bwd_fused(const fa_problem* prob, const void* q, const int64_t* sq,
                      &p));
   p.withhold_arrival = g_withhold_next.exchange(0);
   return launch_bwd_fused(p, dq_accum, stream);
+}
+
+static fa_status check_rotary(const fa_rotary* r, RotaryParams* out) {
+  if (!r) return FA_ERR_NULL;
+  FA_TRY(check_shape(r->B, r->Hq, r->N, r->D, r->dtype));
+  FA_TRY(check_shape(r->B, r->Hkv, r->N, r->D, r->dtype));
+  // rows of a tile of tokens are counted in 32 bits
+  if (r->Hq > (1 << 20) || r->Hkv > (1 << 20)) return FA_ERR_SHAPE;
+  RotaryParams p{};
+  if (r->n_axes < 1 || r->n_axes > 4) return FA_ERR_ARG;
+  int64_t pairs = 0;
+  for (int64_t i = 0; i < r->n_axes; ++i) {
+    if (r->sections[i] < 1 || r->sections[i] > r->D) return FA_ERR_ARG;
+    pairs += r->sections[i];
+    p.sec_end[i] = static_cast<int>(pairs);
+  }
+  if (pairs % 8 != 0 || 2 * pairs > r->D) return FA_ERR_ARG;
+  if (!r->inv_freq || !r->positions) return FA_ERR_NULL;
+  if (reinterpret_cast<uintptr_t>(r->inv_freq) % 4 != 0 ||
+      reinterpret_cast<uintptr_t>(r->positions) % (r->positions_64 ? 8 : 4) != 0)
+    return FA_ERR_ALIGN;
+  for (int i = 0; i < 3; ++i)
+    if (r->pos_stride[i] < 0) return FA_ERR_STRIDE;
+  if ((r->q_weight != nullptr) != (r->k_weight != nullptr)) return FA_ERR_NULL;
+  if (r->q_weight) {
+    const uintptr_t wa = r->weight_f32 || r->dtype == FA_F32 ? 4 : 2;
+    if (reinterpret_cast<uintptr_t>(r->q_weight) % wa != 0 ||
+        reinterpret_cast<uintptr_t>(r->k_weight) % wa != 0)
+      return FA_ERR_ALIGN;
+    if (!(std::isfinite(r->eps) && r->eps >= 0.f)) return FA_ERR_ARG;
+  }
+  p.B = r->B; p.N = r->N; p.Hq = r->Hq; p.Hkv = r->Hkv; p.D = r->D; p.dtype = r->dtype;
+  p.pairs = static_cast<int>(pairs);
+  p.interleaved = r->interleaved ? 1 : 0;
+  p.naxes = static_cast<int>(r->n_axes);
+  p.inv_freq = r->inv_freq; p.pos = r->positions; p.pos64 = r->positions_64 ? 1 : 0;
+  for (int i = 0; i < 3; ++i) p.ps[i] = r->pos_stride[i];
+  p.w[0] = r->q_weight; p.w[1] = r->k_weight;
+  p.w_f32 = r->weight_f32 ? 1 : 0;
+  p.eps = r->eps;
+  *out = p;
+  return FA_OK;
+}
+
+static fa_status rotary_tensor(const RotaryParams& p, int t, const void* x, const int64_t* s,
+                               int64_t* dst) {
+  return check_dense(x, s, p.B, t ? p.Hkv : p.Hq, p.N, p.dtype, dst);
+}
+
+fa_status fa_rotary_fwd(const fa_rotary* rot, const void* q, const int64_t* sq, const void* k,
+                        const int64_t* sk, void* qo, const int64_t* sqo, void* ko,
+                        const int64_t* sko, cudaStream_t stream) {
+  RotaryParams p{};
+  FA_TRY(check_rotary(rot, &p));
+  FA_TRY(rotary_tensor(p, 0, q, sq, p.sx[0]));
+  FA_TRY(rotary_tensor(p, 1, k, sk, p.sx[1]));
+  FA_TRY(rotary_tensor(p, 0, qo, sqo, p.so[0]));
+  FA_TRY(rotary_tensor(p, 1, ko, sko, p.so[1]));
+  DeviceInfo* dev = nullptr;
+  FA_TRY(device_setup(&dev));
+  p.x[0] = q; p.x[1] = k; p.out[0] = qo; p.out[1] = ko;
+  return launch_rotary(p, stream);
+}
+
+size_t fa_rotary_bwd_workspace_bytes(const fa_rotary* rot) {
+  RotaryParams p{};
+  if (check_rotary(rot, &p) != FA_OK || !p.w[0]) return 0;
+  return static_cast<size_t>(kRotaryMaxParts) * 2 * static_cast<size_t>(p.D) * sizeof(float);
+}
+
+fa_status fa_rotary_bwd(const fa_rotary* rot, const void* q, const int64_t* sq, const void* k,
+                        const int64_t* sk, const void* dqo, const int64_t* sdqo, const void* dko,
+                        const int64_t* sdko, void* dq, const int64_t* sdq, void* dk,
+                        const int64_t* sdk, float* dq_weight, float* dk_weight, float* workspace,
+                        size_t workspace_bytes, cudaStream_t stream) {
+  RotaryParams p{};
+  FA_TRY(check_rotary(rot, &p));
+  p.backward = 1;
+  if (p.w[0]) {
+    FA_TRY(rotary_tensor(p, 0, q, sq, p.sin[0]));
+    FA_TRY(rotary_tensor(p, 1, k, sk, p.sin[1]));
+    FA_TRY(check_f32_vec(dq_weight));
+    FA_TRY(check_f32_vec(dk_weight));
+    FA_TRY(check_f32_vec(workspace));
+    if (workspace_bytes < fa_rotary_bwd_workspace_bytes(rot)) return FA_ERR_SCRATCH;
+  }
+  FA_TRY(rotary_tensor(p, 0, dqo, sdqo, p.sx[0]));
+  FA_TRY(rotary_tensor(p, 1, dko, sdko, p.sx[1]));
+  FA_TRY(rotary_tensor(p, 0, dq, sdq, p.so[0]));
+  FA_TRY(rotary_tensor(p, 1, dk, sdk, p.so[1]));
+  DeviceInfo* dev = nullptr;
+  FA_TRY(device_setup(&dev));
+  p.in[0] = q; p.in[1] = k; p.x[0] = dqo; p.x[1] = dko; p.out[0] = dq; p.out[1] = dk;
+  p.dw[0] = dq_weight; p.dw[1] = dk_weight; p.ws = workspace;
+  return launch_rotary(p, stream);
+}
+
+// Everything of a decode problem but its tensors.
+static fa_status check_decode(const fa_decode_problem* pr, DecodeParams* out) {
+  if (!pr) return FA_ERR_NULL;
+  if (pr->dtype != FA_F16 && pr->dtype != FA_BF16) return FA_ERR_DTYPE;
+  if (pr->B < 1 || pr->Hq < 1 || pr->Hkv < 1 || pr->Hq % pr->Hkv != 0) return FA_ERR_SHAPE;
+  if (pr->Nq < 1 || pr->Nq > FA_DECODE_MAX_TOKENS) return FA_ERR_SHAPE;
+  if (pr->P < 0 || pr->S < 0) return FA_ERR_SHAPE;
+  const int64_t D = pr->D;
+  if (D != 16 && D != 32 && D != 64 && D != 128) return FA_ERR_HEADDIM;
+  // rows and blocks are counted in 32 bits; TMA rows run up to a tile past P
+  const int64_t row_max = (int64_t)INT32_MAX - 1024;
+  int64_t t, u;
+  if (!mul_ok(pr->B, pr->Hq, &t) || !mul_ok(t, pr->Nq, &t) || t > row_max) return FA_ERR_SHAPE;
+  if (pr->P > row_max || pr->S > row_max) return FA_ERR_SHAPE;
+  if (!mul_ok(pr->B, pr->Hkv, &u) || !mul_ok(u, pr->S, &u) || !mul_ok(u, D * 8, &u))
+    return FA_ERR_SHAPE;
+  if (!mul_ok(pr->Hkv, pr->P, &u) || !mul_ok(u, D * 8, &u)) return FA_ERR_SHAPE;
+  FA_TRY(check_scale(pr->scale));
+  if (pr->S > 0) {
+    if (!pr->seq_lens) return FA_ERR_NULL;
+    if (reinterpret_cast<uintptr_t>(pr->seq_lens) % 4 != 0) return FA_ERR_ALIGN;
+  }
+  DecodeParams p{};
+  p.B = pr->B; p.Hkv = pr->Hkv; p.G = pr->Hq / pr->Hkv; p.Nq = pr->Nq; p.D = D;
+  p.P = pr->P; p.S = pr->S; p.lens = pr->seq_lens;
+  p.causal = pr->causal ? 1 : 0; p.scale = pr->scale; p.dtype = pr->dtype;
+  *out = p;
+  return FA_OK;
+}
+
+size_t fa_decode_workspace_bytes(const fa_decode_problem* prob) {
+  DecodeParams p{};
+  if (check_decode(prob, &p) != FA_OK) return 0;
+  const PrefixPlan pl = decode_plan(p.B, p.Hkv, p.G * p.Nq, p.D, p.P);
+  // per range of the prefix and query row: D sums and a log-sum-exp
+  return static_cast<size_t>(pl.ns) * static_cast<size_t>(p.Hkv * p.B * p.G * p.Nq) *
+         static_cast<size_t>(p.D + 1) * sizeof(float);
+}
+
+fa_status fa_decode(const fa_decode_problem* prob, const void* q, const int64_t* sq,
+                    const void* k_prefix, const int64_t* skp, const void* v_prefix,
+                    const int64_t* svp, const void* k, const int64_t* sk, const void* v,
+                    const int64_t* sv, void* o, const int64_t* so, float* lse, float* workspace,
+                    size_t workspace_bytes, cudaStream_t stream) {
+  DecodeParams p{};
+  FA_TRY(check_decode(prob, &p));
+  const int64_t Hq = p.Hkv * p.G;
+  FA_TRY(check_dense(q, sq, p.B, Hq, p.Nq, p.dtype, p.sq));
+  if (p.P > 0) {
+    FA_TRY(check_dense(k_prefix, skp, 1, p.Hkv, p.P, p.dtype, p.skp));
+    FA_TRY(check_dense(v_prefix, svp, 1, p.Hkv, p.P, p.dtype, p.svp));
+  }
+  if (p.S > 0) {
+    FA_TRY(check_dense(k, sk, p.B, p.Hkv, p.S, p.dtype, p.sk));
+    FA_TRY(check_dense(v, sv, p.B, p.Hkv, p.S, p.dtype, p.sv));
+  }
+  FA_TRY(check_dense(o, so, p.B, Hq, p.Nq, p.dtype, p.so));
+  FA_TRY(check_f32_vec(lse));
+  const size_t need = fa_decode_workspace_bytes(prob);
+  if (need > 0) {
+    FA_TRY(check_f32_vec(workspace));
+    if (workspace_bytes < need) return FA_ERR_SCRATCH;
+  }
+  DeviceInfo* dev = nullptr;
+  FA_TRY(device_setup(&dev));
+  p.q = q; p.kp = k_prefix; p.vp = v_prefix; p.k = k; p.v = v; p.o = o; p.lse = lse;
+  p.ws = workspace;
+  p.status = dev->status; p.timeout_ns = g_timeout_ns.load();
+  return launch_decode(p, stream);
 }
 
 fa_status fa_get_device_status(cudaStream_t stream) {

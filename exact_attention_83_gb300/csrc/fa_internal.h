@@ -195,6 +195,54 @@ __device__ __forceinline__ void tile_keep_bits(const Dropout& d, int64_t bh, int
 }
 #endif
 
+// Parameters of one rotation call (fa_rotary_*), tensor 0 = queries, 1 = keys.
+struct RotaryParams {
+  const void* x[2];          // forward: the inputs; gradient: the incoming gradients
+  const void* in[2];         // gradient of the norm: the forward's inputs
+  void* out[2];
+  int64_t sx[2][4], sin[2][4], so[2][4];
+  int64_t B, N, Hq, Hkv, D;
+  fa_dtype dtype;
+  int pairs, interleaved, naxes, sec_end[4];
+  const float* inv_freq;
+  const void* pos;
+  int pos64;
+  int64_t ps[3];
+  const void* w[2];          // norm weights, or null (no norm)
+  int w_f32;
+  float eps;
+  int backward;
+  float* dw[2];
+  float* ws;                 // kRotaryMaxParts * 2 * D floats
+};
+// Blocks of the norm's gradient, each of which leaves one partial row of the
+// weight gradients: three per SM.
+constexpr int kRotaryMaxParts = 456;
+fa_status launch_rotary(const RotaryParams& p, cudaStream_t s);
+
+// Parameters of one fa_decode call.
+struct DecodeParams {
+  const void* q; const void* kp; const void* vp; const void* k; const void* v;
+  void* o; float* lse;
+  int64_t B, Hkv, G, Nq, D, P, S;
+  int64_t sq[4], skp[4], svp[4], sk[4], sv[4], so[4];
+  const int32_t* lens;
+  int causal;
+  float scale;
+  fa_dtype dtype;
+  float* ws;
+  unsigned int* status;
+  uint64_t timeout_ns;
+};
+// How fa_decode cuts the prefix: ns ranges of key tiles (0: no prefix), row
+// groups of 256 (two = 1) or 128 query rows.
+struct PrefixPlan {
+  int ns, two;
+  int64_t groups;
+};
+PrefixPlan decode_plan(int64_t B, int64_t Hkv, int64_t GN, int64_t D, int64_t P);
+fa_status launch_decode(const DecodeParams& p, cudaStream_t s);
+
 // Records prof[i] on s when profiling events are set.
 inline void prof_record(const BwdParams& p, int i, cudaStream_t s) {
   if (p.prof) cudaEventRecord(p.prof[i], s);

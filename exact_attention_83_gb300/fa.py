@@ -39,6 +39,24 @@ keep-mask buffer that the backward reads).
   attention(q, k, v, causal, scale, dropout_p=..., seed=..., offset=...)
   attention_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
                    max_seqlen_k, causal, scale, dropout_p, seed, offset)
+Rotation of query and key heads by positions with one or several axes, and the
+RMS norm of every head in the same pass (fa_rotary_fwd / fa_rotary_bwd):
+  rotary(q, k, positions, inv_freq, sections, interleaved)      -> (q', k') with autograd
+  qk_norm_rotary(q, k, q_weight, k_weight, positions, inv_freq, sections,
+                 interleaved, eps)                              -> (q', k') with autograd
+  rotary_fwd / rotary_bwd, qk_norm_rotary_fwd / qk_norm_rotary_bwd: the same with
+                                    outputs allocated (or given as out=)
+  Rotary(...)                       the same choices as one value, which
+                                    attention_gqa(..., rotary=) and
+                                    attention_varlen(..., rotary=) apply first
+
+Serving (fa_decode): the newest tokens of a batch whose keys are a prefix that
+all requests share, followed by each request's own cache rows:
+  attention_decode(q, k_prefix, v_prefix, k, v, seq_lens, causal, scale)
+                                    -> (o, lse)   allocates outputs and workspace
+  decode(q, k_prefix, v_prefix, k, v, seq_lens, o, lse, causal, scale, *, workspace)
+  decode_workspace_bytes(q, k_prefix, k)
+
 Fixed lengths: q, o, do [B, Hq, Nq, D]; k, v [B, Hkv, Nk, D]; lse [B, Hq, Nq].
 Packed: q, o, do [total_q, Hq, D]; k, v [total_k, Hkv, D]; lse [Hq, total_q];
 cu_seqlens_* int32 CUDA tensors of B+1 offsets, max_seqlen_* host ints.
@@ -50,6 +68,7 @@ import ctypes
 import math
 import os
 import threading
+from typing import NamedTuple, Optional, Sequence
 
 import torch
 
@@ -72,7 +91,9 @@ EXPORTED = ("fa_fwd", "fa_bwd_preprocess", "fa_bwd", "fa_get_device_status",
             "fa_set_profile_events", "fa_version", "fa_bwd_noalloc",
             "fa_test_withhold_next_arrival", "fa_fwd_ex", "fa_bwd_ex",
             "fa_bwd_fused_workspace_bytes", "fa_bwd_fused", "fa_dropout_mask_bytes",
-            "fa_dropout_mask", "fa_test_set_l2_bytes")
+            "fa_dropout_mask", "fa_test_set_l2_bytes", "fa_rotary_fwd",
+            "fa_rotary_bwd_workspace_bytes", "fa_rotary_bwd", "fa_decode_workspace_bytes",
+            "fa_decode")
 
 
 class Problem(ctypes.Structure):
@@ -84,6 +105,26 @@ class Problem(ctypes.Structure):
                 ("causal", ctypes.c_int), ("scale", ctypes.c_float), ("dtype", ctypes.c_int),
                 ("dropout_p", ctypes.c_float), ("seed", ctypes.c_uint64),
                 ("offset", ctypes.c_uint32), ("dropout_mask", ctypes.c_void_p)]
+
+
+class RotaryProblem(ctypes.Structure):
+    """struct fa_rotary of include/fa.h."""
+    _fields_ = [("B", ctypes.c_int64), ("N", ctypes.c_int64), ("Hq", ctypes.c_int64),
+                ("Hkv", ctypes.c_int64), ("D", ctypes.c_int64), ("dtype", ctypes.c_int),
+                ("interleaved", ctypes.c_int), ("n_axes", ctypes.c_int64),
+                ("sections", ctypes.c_int64 * 4), ("inv_freq", ctypes.c_void_p),
+                ("positions", ctypes.c_void_p), ("pos_stride", ctypes.c_int64 * 3),
+                ("positions_64", ctypes.c_int), ("weight_f32", ctypes.c_int),
+                ("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("eps", ctypes.c_float)]
+
+
+class DecodeProblem(ctypes.Structure):
+    """struct fa_decode_problem of include/fa.h."""
+    _fields_ = [("B", ctypes.c_int64), ("Hq", ctypes.c_int64), ("Hkv", ctypes.c_int64),
+                ("Nq", ctypes.c_int64), ("D", ctypes.c_int64), ("P", ctypes.c_int64),
+                ("S", ctypes.c_int64), ("seq_lens", ctypes.c_void_p), ("causal", ctypes.c_int),
+                ("scale", ctypes.c_float), ("dtype", ctypes.c_int)]
 
 
 class FAError(RuntimeError):
@@ -140,6 +181,20 @@ def load_library(path: str = LIB_PATH):
         lib.fa_dropout_mask_bytes.restype = ctypes.c_size_t
         lib.fa_dropout_mask.argtypes = [_pp, _vp, ctypes.c_size_t, _vp]
         lib.fa_dropout_mask.restype = ctypes.c_int
+        _pr = ctypes.POINTER(RotaryProblem)
+        lib.fa_rotary_fwd.argtypes = [_pr, _vp, _s4, _vp, _s4, _vp, _s4, _vp, _s4, _vp]
+        lib.fa_rotary_fwd.restype = ctypes.c_int
+        lib.fa_rotary_bwd_workspace_bytes.argtypes = [_pr]
+        lib.fa_rotary_bwd_workspace_bytes.restype = ctypes.c_size_t
+        lib.fa_rotary_bwd.argtypes = [_pr, _vp, _s4, _vp, _s4, _vp, _s4, _vp, _s4, _vp, _s4, _vp,
+                                      _s4, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+        lib.fa_rotary_bwd.restype = ctypes.c_int
+        _pd = ctypes.POINTER(DecodeProblem)
+        lib.fa_decode_workspace_bytes.argtypes = [_pd]
+        lib.fa_decode_workspace_bytes.restype = ctypes.c_size_t
+        lib.fa_decode.argtypes = [_pd, _vp, _s4, _vp, _s4, _vp, _s4, _vp, _s4, _vp, _s4, _vp, _s4,
+                                  _vp, _vp, ctypes.c_size_t, _vp]
+        lib.fa_decode.restype = ctypes.c_int
         lib.fa_get_device_status.argtypes = [_vp]
         lib.fa_get_device_status.restype = ctypes.c_int
         lib.fa_status_string.argtypes = [ctypes.c_int]
@@ -322,6 +377,297 @@ def attention(q, k, v, causal: bool = False, scale=None):
     """Exact softmax attention with autograd.  Second-order gradients are
     refused (once_differentiable raises) rather than silently wrong."""
     return _Attention.apply(q, k, v, causal, scale)
+
+
+# ----------------------------------------------------------------------------
+# Rotation of query and key heads by their positions, and their norm
+
+
+class Rotary(NamedTuple):
+    """A rotation (and, with weights, a head norm) of queries and keys.
+
+    positions: int32 or int64 CUDA tensor.  Beside [B, H, N, D] heads: [A, B, N]
+    for A axes ([A, 1, N] shares them over the batch; with one axis also [B, N]
+    or [N]); beside packed [T, H, D] heads: [A, T], or [T] with one axis.
+    inv_freq: float32 CUDA vector, one frequency per rotated pair (a multiple of
+    8 of them, at most D / 2).  sections: rotated pairs of each axis, in the
+    order of inv_freq (None: one axis).  interleaved: pairs (2i, 2i + 1) instead
+    of (i, n + i).  q_weight, k_weight: norm weights of D elements, float32 or
+    the heads' type (None: no norm); eps: the norm's."""
+    positions: torch.Tensor
+    inv_freq: torch.Tensor
+    sections: Optional[Sequence[int]] = None
+    interleaved: bool = False
+    q_weight: Optional[torch.Tensor] = None
+    k_weight: Optional[torch.Tensor] = None
+    eps: float = 1e-6
+
+
+def _rotary_problem(q, k, rot: Rotary):
+    """struct fa_rotary of a call, and whether the tensors are packed."""
+    if q.dtype not in _DTYPE_CODE or not q.is_cuda:
+        raise TypeError("tensors must be CUDA float32, float16 or bfloat16")
+    if q.dim() not in (3, 4) or k.dim() != q.dim():
+        raise ValueError("expected [B, H, N, D] or packed [T, H, D] tensors")
+    if k.dtype != q.dtype or k.device != q.device or k.shape[-1] != q.shape[-1]:
+        raise ValueError("q and k must share dtype, device and head dimension")
+    packed = q.dim() == 3
+    q4, k4 = _as4(q, packed), _as4(k, packed)
+    B, Hq, N, D = q4.shape
+    if k4.shape[0] != B or k4.shape[2] != N:
+        raise ValueError("q and k must share batch and length")
+    pos, freq = rot.positions, rot.inv_freq
+    if freq.dtype != torch.float32 or freq.device != q.device or freq.dim() != 1 \
+            or not freq.is_contiguous():
+        raise ValueError("inv_freq: a contiguous float32 vector on q's device")
+    if pos.dtype not in (torch.int32, torch.int64) or pos.device != q.device:
+        raise ValueError("positions: int32 or int64 on q's device")
+    sections = [freq.numel()] if rot.sections is None else [int(n) for n in rot.sections]
+    A = len(sections)
+    if A < 1 or A > 4 or sum(sections) != freq.numel():
+        raise ValueError("sections: one to four counts that add up to inv_freq's length")
+    # one axis may leave out the axis dimension, and a batch shared positions
+    full = 2 if packed else 3
+    if pos.dim() < full and A == 1:
+        pos = pos[None]
+    if pos.dim() == 2 and not packed:
+        pos = pos[:, None] if pos.shape[0] == A and A == 1 else pos
+    want = (A, N) if packed else (A, B, N)
+    if pos.dim() != full or any(p != w and not (i == 1 and not packed and p == 1)
+                                for i, (p, w) in enumerate(zip(pos.shape, want))):
+        raise ValueError(f"positions: expected {list(want)}, got {list(rot.positions.shape)}")
+    if packed:
+        pos = pos[:, None]
+    pr = RotaryProblem()
+    pr.B, pr.N, pr.Hq, pr.Hkv, pr.D = B, N, Hq, k4.shape[1], D
+    pr.dtype, pr.interleaved = _DTYPE_CODE[q.dtype], int(bool(rot.interleaved))
+    pr.n_axes = A
+    for i, n in enumerate(sections):
+        pr.sections[i] = n
+    pr.inv_freq, pr.positions = freq.data_ptr(), pos.data_ptr()
+    pr.positions_64 = int(pos.dtype == torch.int64)
+    for i in range(3):
+        pr.pos_stride[i] = pos.stride(i) if pos.shape[i] > 1 else 0
+    if (rot.q_weight is None) != (rot.k_weight is None):
+        raise ValueError("q_weight and k_weight: both or none")
+    if rot.q_weight is not None:
+        for w in (rot.q_weight, rot.k_weight):
+            if w.device != q.device or tuple(w.shape) != (D,) or not w.is_contiguous() \
+                    or w.dtype not in (torch.float32, q.dtype) or w.dtype != rot.q_weight.dtype:
+                raise ValueError("q_weight, k_weight: contiguous [D] of one dtype, float32 or q's")
+        pr.q_weight, pr.k_weight = rot.q_weight.data_ptr(), rot.k_weight.data_ptr()
+        pr.weight_f32 = int(rot.q_weight.dtype == torch.float32)
+    pr.eps = float(rot.eps)
+    return pr, packed
+
+
+def _rotary_out(x, out):
+    if out is None:
+        return torch.empty_like(x, memory_format=torch.contiguous_format)
+    if out.shape != x.shape or out.dtype != x.dtype or out.device != x.device:
+        raise ValueError("out: the shape, dtype and device of its input")
+    return out
+
+
+def _apply_fwd(q, k, rot, out):
+    pr, packed = _rotary_problem(q, k, rot)
+    qo, ko = (_rotary_out(x, o) for x, o in zip((q, k), out or (None, None)))
+    t4 = [_as4(t, packed) for t in (q, k, qo, ko)]
+    lib = load_library()
+    with torch.cuda.device(q.device):
+        code = lib.fa_rotary_fwd(ctypes.byref(pr), *(a for t in t4 for a in (t.data_ptr(), _strides(t))),
+                                 _stream(q))
+    _check(code, "fa_rotary_fwd")
+    return qo, ko
+
+
+def _apply_bwd(q, k, dqo, dko, rot, out):
+    """q, k are not read when rot has no weights (and may be the gradients)."""
+    pr, packed = _rotary_problem(dqo, dko, rot)
+    norm = rot.q_weight is not None
+    if norm:
+        for x, g in ((q, dqo), (k, dko)):
+            if x.shape != g.shape or x.dtype != g.dtype or x.device != g.device:
+                raise ValueError("gradients: the shape, dtype and device of their inputs")
+    dq, dk = (_rotary_out(x, o) for x, o in zip((dqo, dko), out or (None, None)))
+    D = dqo.shape[-1]
+    lib = load_library()
+    dw = ws = None
+    nbytes = 0
+    if norm:
+        dw = torch.empty((2, D), dtype=torch.float32, device=q.device)
+        nbytes = int(lib.fa_rotary_bwd_workspace_bytes(ctypes.byref(pr)))
+        ws = torch.empty(max(nbytes // 4, 4), dtype=torch.float32, device=q.device)
+    t4 = [_as4(t, packed) for t in (q if norm else dqo, k if norm else dko, dqo, dko, dq, dk)]
+    with torch.cuda.device(dqo.device):
+        code = lib.fa_rotary_bwd(ctypes.byref(pr),
+                                 *(a for t in t4 for a in (t.data_ptr(), _strides(t))),
+                                 dw[0].data_ptr() if norm else None,
+                                 dw[1].data_ptr() if norm else None,
+                                 ws.data_ptr() if norm else None, nbytes, _stream(dqo))
+    _check(code, "fa_rotary_bwd")
+    return (dq, dk, dw[0], dw[1]) if norm else (dq, dk)
+
+
+def rotary_fwd(q, k, positions, inv_freq, sections=None, interleaved: bool = False, out=None):
+    """fa_rotary_fwd without a norm: (q', k'), the heads rotated by their
+    positions (see Rotary).  q [B, Hq, N, D], k [B, Hkv, N, D], or packed
+    [T, H, D].  out: the two tensors to write, which may be q and k themselves."""
+    return _apply_fwd(q, k, Rotary(positions, inv_freq, sections, interleaved), out)
+
+
+def rotary_bwd(dq_out, dk_out, positions, inv_freq, sections=None, interleaved: bool = False,
+               out=None):
+    """fa_rotary_bwd without a norm: (dq, dk) from the gradients of rotary_fwd's
+    outputs.  out: the two tensors to write, which may be the gradients themselves."""
+    return _apply_bwd(None, None, dq_out, dk_out, Rotary(positions, inv_freq, sections, interleaved),
+                      out)
+
+
+def qk_norm_rotary_fwd(q, k, q_weight, k_weight, positions, inv_freq, sections=None,
+                       interleaved: bool = False, eps: float = 1e-6, out=None):
+    """fa_rotary_fwd with the RMS norm of every head before the rotation."""
+    return _apply_fwd(q, k, Rotary(positions, inv_freq, sections, interleaved, q_weight, k_weight,
+                                   eps), out)
+
+
+def qk_norm_rotary_bwd(q, k, q_weight, k_weight, dq_out, dk_out, positions, inv_freq,
+                       sections=None, interleaved: bool = False, eps: float = 1e-6, out=None):
+    """fa_rotary_bwd with the norm: (dq, dk, dq_weight, dk_weight), the weight
+    gradients in float32."""
+    return _apply_bwd(q, k, dq_out, dk_out, Rotary(positions, inv_freq, sections, interleaved,
+                                                   q_weight, k_weight, eps), out)
+
+
+def _dense(t: torch.Tensor) -> torch.Tensor:
+    """t, or a contiguous copy when its layout is not one the kernels take
+    (e.g. the expanded gradient of a sum)."""
+    es = t.element_size()
+    ok = t.stride(-1) == 1 and t.data_ptr() % 16 == 0 and all(
+        n == 1 or (s > 0 and s * es % 16 == 0) for n, s in zip(t.shape[:-1], t.stride()[:-1]))
+    return t if ok else t.contiguous()
+
+
+class _ApplyRotary(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, q_weight, k_weight, rot):
+        norm = q_weight is not None
+        ctx.rot = rot._replace(q_weight=None, k_weight=None)
+        # without a norm the gradient needs no input
+        ctx.save_for_backward(*((q, k, q_weight, k_weight) if norm else ()))
+        return _apply_fwd(q, k, rot, None)
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, dqo, dko):
+        dqo, dko = _dense(dqo), _dense(dko)
+        if not ctx.saved_tensors:
+            return (*_apply_bwd(None, None, dqo, dko, ctx.rot, None), None, None, None)
+        q, k, qw, kw = ctx.saved_tensors
+        dq, dk, dqw, dkw = _apply_bwd(q, k, dqo, dko, ctx.rot._replace(q_weight=qw, k_weight=kw),
+                                      None)
+        return dq, dk, dqw.to(qw.dtype), dkw.to(kw.dtype), None
+
+
+def apply_rotary(q, k, rot: Rotary):
+    """(q', k') of a Rotary, with autograd for q, k and the norm's weights.
+    Second-order gradients are refused."""
+    return _ApplyRotary.apply(_dense(q), _dense(k), rot.q_weight, rot.k_weight, rot)
+
+
+def rotary(q, k, positions, inv_freq, sections=None, interleaved: bool = False):
+    """rotary_fwd with autograd."""
+    return apply_rotary(q, k, Rotary(positions, inv_freq, sections, interleaved))
+
+
+def qk_norm_rotary(q, k, q_weight, k_weight, positions, inv_freq, sections=None,
+                   interleaved: bool = False, eps: float = 1e-6):
+    """qk_norm_rotary_fwd with autograd."""
+    return apply_rotary(q, k, Rotary(positions, inv_freq, sections, interleaved, q_weight, k_weight,
+                                     eps))
+
+
+# ----------------------------------------------------------------------------
+# Serving: new tokens over a shared prefix and each request's own rows
+
+
+def _decode_problem(q, k_prefix, k, seq_lens, causal, scale):
+    if q.dtype not in (torch.float16, torch.bfloat16) or not q.is_cuda:
+        raise TypeError("decode takes CUDA float16 or bfloat16 tensors")
+    if q.dim() != 4 or k.dim() != 4 or k_prefix.dim() != 3:
+        raise ValueError("expected q [B, Hq, Nq, D], k, v [B, Hkv, S, D], prefixes [Hkv, P, D]")
+    B, Hq, Nq, D = q.shape
+    if k.shape[0] != B or k.shape[3] != D or k_prefix.shape[0] != k.shape[1] \
+            or k_prefix.shape[2] != D:
+        raise ValueError("q, k and the prefix must share batch, key/value heads and head dimension")
+    pr = DecodeProblem()
+    pr.B, pr.Hq, pr.Hkv, pr.Nq, pr.D = B, Hq, k.shape[1], Nq, D
+    pr.P, pr.S = k_prefix.shape[1], k.shape[2]
+    if seq_lens is not None:
+        if seq_lens.dtype != torch.int32 or tuple(seq_lens.shape) != (B,) \
+                or seq_lens.device != q.device or not seq_lens.is_contiguous():
+            raise ValueError("seq_lens: a contiguous int32 vector of B lengths on q's device")
+        pr.seq_lens = seq_lens.data_ptr()
+    pr.causal, pr.scale, pr.dtype = int(bool(causal)), _scale(D, scale), _DTYPE_CODE[q.dtype]
+    return pr
+
+
+def decode_workspace_bytes(q, k_prefix, k) -> int:
+    """Bytes of the workspace decode needs for these shapes (0 if invalid, or
+    without a prefix)."""
+    pr = _decode_problem(q, k_prefix, k, None, True, None)
+    pr.seq_lens = 16           # its contents do not matter here
+    return int(load_library().fa_decode_workspace_bytes(ctypes.byref(pr)))
+
+
+def decode(q, k_prefix, v_prefix, k, v, seq_lens, o, lse, causal: bool = True, scale=None, *,
+           workspace: Optional[torch.Tensor] = None):
+    """fa_decode.  workspace: a contiguous CUDA tensor of at least
+    decode_workspace_bytes(q, k_prefix, k) bytes, 16-byte aligned (None when
+    that is 0); calls that may overlap on the GPU need one each."""
+    pr = _decode_problem(q, k_prefix, k, seq_lens, causal, scale)
+    for ref, ts in ((q, (o,)), (k, (v,)), (k_prefix, (v_prefix,))):
+        for t in ts:
+            if t.shape != ref.shape:
+                raise ValueError("o, v and v_prefix take the shapes of q, k and k_prefix")
+    for t in (k_prefix, v_prefix, k, v, o):
+        if t.dtype != q.dtype or t.device != q.device:
+            raise ValueError("all tensors must share dtype and device")
+    if lse.dtype != torch.float32 or lse.shape != q.shape[:3] or lse.device != q.device \
+            or not lse.is_contiguous():
+        raise ValueError("lse: contiguous float32 [B, Hq, Nq] on q's device")
+    nbytes = 0
+    if workspace is not None:
+        if workspace.device != q.device or not workspace.is_contiguous():
+            raise ValueError("workspace: a contiguous tensor on q's device")
+        nbytes = workspace.numel() * workspace.element_size()
+    lib = load_library()
+    args = []
+    for t in (q, k_prefix[None], v_prefix[None], k, v, o):
+        args += [t.data_ptr(), _strides(t)]
+    with torch.cuda.device(q.device):
+        code = lib.fa_decode(ctypes.byref(pr), *args, lse.data_ptr(),
+                             workspace.data_ptr() if workspace is not None else None, nbytes,
+                             _stream(q))
+    _check(code, "fa_decode")
+
+
+def attention_decode(q, k_prefix, v_prefix, k, v, seq_lens, causal: bool = True, scale=None,
+                     workspace: Optional[torch.Tensor] = None):
+    """Attention of the newest Nq (1 to 16) tokens of B requests: returns
+    (o [B, Hq, Nq, D], lse [B, Hq, Nq]).  q [B, Hq, Nq, D]; k_prefix, v_prefix
+    [Hkv, P, D], keys that every request sees in full; k, v [B, Hkv, S, D], the
+    requests' own cache rows, of which request b's first seq_lens[b] count (int32
+    CUDA vector; the new tokens' rows among them, as the last Nq).  causal: token
+    t sees own rows up to its own.  float16 and bfloat16; no gradient."""
+    o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+    if workspace is None:
+        nbytes = decode_workspace_bytes(q, k_prefix, k)
+        if nbytes:
+            workspace = torch.empty(nbytes // 4, dtype=torch.float32, device=q.device)
+    decode(q, k_prefix, v_prefix, k, v, seq_lens, o, lse, causal, scale, workspace=workspace)
+    return o, lse
 
 
 # ----------------------------------------------------------------------------
@@ -560,12 +906,16 @@ class _AttentionEx(torch.autograd.Function):
 
 def attention_gqa(q, k, v, causal: bool = False, scale=None, dropout_p: float = 0.0,
                   seed: int = 0, offset: int = 0, deterministic: bool = True,
-                  keep_mask: bool | None = None):
+                  keep_mask: bool | None = None, rotary: Optional[Rotary] = None):
     """Autograd attention for q [B, Hq, Nq, D], k, v [B, Hkv, Nk, D] (Hq % Hkv == 0),
     with optional dropout of the attention weights.  deterministic=False takes
     the single-pass backward (dQ not bitwise reproducible).  keep_mask: let
     the forward store its dropout decisions in a buffer the backward reads
-    (True), never (False), or when it fits DROPOUT_MASK_AUTO_BYTES (None)."""
+    (True), never (False), or when it fits DROPOUT_MASK_AUTO_BYTES (None).
+    rotary: the rotation (and head norm) to apply to q and k first; they need
+    one length then."""
+    if rotary is not None:
+        q, k = apply_rotary(q, k, rotary)
     kw = dict(dropout_p=dropout_p, seed=seed, offset=offset)
     return _AttentionEx.apply(q, k, v, causal, scale, kw, deterministic, keep_mask)
 
@@ -573,10 +923,13 @@ def attention_gqa(q, k, v, causal: bool = False, scale=None, dropout_p: float = 
 def attention_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int,
                      max_seqlen_k: int, causal: bool = False, scale=None,
                      dropout_p: float = 0.0, seed: int = 0, offset: int = 0,
-                     deterministic: bool = True, keep_mask: bool | None = None):
+                     deterministic: bool = True, keep_mask: bool | None = None,
+                     rotary: Optional[Rotary] = None):
     """Autograd attention over packed sequences: q [total_q, Hq, D],
     k, v [total_k, Hkv, D], cu_seqlens_* int32 CUDA offsets (B+1); keep_mask
-    as for attention_gqa."""
+    and rotary as for attention_gqa."""
+    if rotary is not None:
+        q, k = apply_rotary(q, k, rotary)
     kw = dict(cu_seqlens_q=cu_seqlens_q, cu_seqlens_k=cu_seqlens_k,
               max_seqlen_q=max_seqlen_q, max_seqlen_k=max_seqlen_k,
               dropout_p=dropout_p, seed=seed, offset=offset)

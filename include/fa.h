@@ -334,6 +334,126 @@ FA_API fa_status fa_dropout_mask(const fa_problem* prob, uint8_t* mask, size_t b
                                  cudaStream_t stream);
 
 /*
+ * Rotation of query and key heads by their positions, with one or several
+ * axes, and optionally the RMS norm of every head in the same pass.
+ *
+ *   B, N, Hq, Hkv, D, dtype
+ *              q, qo are [B, Hq, N, D], k, ko are [B, Hkv, N, D]; packed rows
+ *              [T, H, D] are the case B = 1, N = T.  Hq and Hkv need not divide
+ *              one another.
+ *   n_axes, sections
+ *              1..4 axes; the n = sum(sections) rotated pairs of every head
+ *              take their position from axis 0 (the first sections[0] pairs),
+ *              axis 1 (the next sections[1]), ...  n must be a multiple of 8
+ *              and 2 n <= D; elements 2 n .. D-1 are not rotated.
+ *   interleaved  0: pair i is elements (i, n + i);  1: (2 i, 2 i + 1)
+ *   inv_freq   DEVICE array of n fp32 frequencies (finite): the angle of pair i
+ *              is positions[axis of i] * inv_freq[i], in radians, formed without
+ *              rounding the product (a position far into a long context keeps
+ *              its angle; exact enough for |position| < 2^36)
+ *   positions, positions_64, pos_stride
+ *              DEVICE array of int32 (positions_64 = 0) or int64 positions, with
+ *              element strides in the order (axis, b, n); a stride of 0 shares
+ *              positions along that dimension
+ *   q_weight, k_weight, weight_f32, eps
+ *              both NULL: rotation only.  Both set: DEVICE arrays of D weights
+ *              (fp32 when weight_f32, else of type dtype); each head x is first
+ *              replaced by  x * rstd * weight,  rstd = (sum x^2 / D + eps)^(-1/2),
+ *              eps finite and >= 0.
+ *
+ * fa_rotary_fwd writes qo and ko:  a' = a cos - b sin,  b' = a sin + b cos  for
+ * each pair (a, b).  All arithmetic is fp32, rounded to dtype once at the end.
+ *
+ * fa_rotary_bwd writes dq and dk from the gradients dqo and dko of the outputs.
+ * With a norm it also reads the forward's q and k and writes dq_weight and
+ * dk_weight (fp32, D values each, 16-byte aligned), summed in a fixed order
+ * through `workspace` (DEVICE, 16-byte aligned, at least
+ * fa_rotary_bwd_workspace_bytes(rot) bytes, which may be reused once the call's
+ * work has finished); without one q, k, dq_weight, dk_weight and workspace are
+ * ignored and may be NULL.
+ *
+ * An output may be the input of the same shape itself (same base, same
+ * strides); otherwise outputs must not overlap anything.  Errors: FA_ERR_NULL,
+ * FA_ERR_SHAPE, FA_ERR_HEADDIM, FA_ERR_DTYPE, FA_ERR_ALIGN and FA_ERR_STRIDE as
+ * for fa_fwd (a stride of 0 over more than one row or head is FA_ERR_STRIDE,
+ * also for inputs); FA_ERR_ARG for n_axes, sections or eps out of range;
+ * FA_ERR_SCRATCH for a workspace that is too small.
+ */
+typedef struct fa_rotary {
+  int64_t B, N, Hq, Hkv, D;
+  fa_dtype dtype;
+  int interleaved;
+  int64_t n_axes;
+  int64_t sections[4];
+  const float* inv_freq;
+  const void* positions;
+  int64_t pos_stride[3];
+  int positions_64;
+  int weight_f32;
+  const void* q_weight;
+  const void* k_weight;
+  float eps;
+} fa_rotary;
+
+FA_API fa_status fa_rotary_fwd(const fa_rotary* rot, const void* q, const int64_t* sq,
+                               const void* k, const int64_t* sk, void* qo, const int64_t* sqo,
+                               void* ko, const int64_t* sko, cudaStream_t stream);
+FA_API size_t fa_rotary_bwd_workspace_bytes(const fa_rotary* rot);
+FA_API fa_status fa_rotary_bwd(const fa_rotary* rot, const void* q, const int64_t* sq,
+                               const void* k, const int64_t* sk, const void* dqo,
+                               const int64_t* sdqo, const void* dko, const int64_t* sdko, void* dq,
+                               const int64_t* sdq, void* dk, const int64_t* sdk, float* dq_weight,
+                               float* dk_weight, float* workspace, size_t workspace_bytes,
+                               cudaStream_t stream);
+
+/*
+ * Attention of the newest tokens of B requests (one token each, or a few
+ * drafted ones) whose keys are one prefix that all requests share, followed by
+ * each request's own cache rows.  The prefix is read once for the whole batch.
+ * fp16 and bf16.
+ *
+ *   B, Hq, Hkv  requests; query and key/value heads (Hq % Hkv == 0, grouped as
+ *              for fa_problem)
+ *   Nq         new tokens per request, 1 .. FA_DECODE_MAX_TOKENS
+ *   P          prefix keys, >= 0 (0: no prefix; k_prefix, v_prefix are ignored)
+ *   S          rows allocated per request, >= 0 (0: prefix only; k, v and
+ *              seq_lens are ignored)
+ *   seq_lens   DEVICE array of B int32: request b's own keys are rows
+ *              0 .. seq_lens[b] - 1 of k, v (the new tokens among them).  Rows
+ *              past them are not read.  A length below 0 or above S skips the
+ *              request (its outputs are left as they were) and records
+ *              FA_ERR_SEQLENS.
+ *   causal     token t sees own rows j <= seq_lens[b] - Nq + t (the new tokens
+ *              are the last Nq own rows); 0: every token sees all own rows
+ *
+ * q, o are [B, Hq, Nq, D]; k_prefix, v_prefix [1, Hkv, P, D]; k, v
+ * [B, Hkv, S, D], with 4 element strides each in the order (b, h, n, d) as for
+ * fa_fwd, but no stride of 0 over an extent above 1.  lse is contiguous fp32
+ * [B, Hq, Nq].  A token that sees no key at all gets o = 0 and lse = -inf.
+ * `workspace` (DEVICE, 16-byte aligned, fa_decode_workspace_bytes(prob) bytes)
+ * holds partial sums; it may be reused once the call's work has finished, and
+ * calls that overlap on the GPU need one each.  Nothing in it needs to be set.
+ * P is rounded to the input type before P V, as by fa_fwd.
+ *
+ * Errors as for fa_fwd_ex, plus FA_ERR_DTYPE for FA_F32 and FA_ERR_SCRATCH.
+ */
+#define FA_DECODE_MAX_TOKENS 16
+typedef struct fa_decode_problem {
+  int64_t B, Hq, Hkv, Nq, D, P, S;
+  const int32_t* seq_lens;
+  int causal;
+  float scale;
+  fa_dtype dtype;
+} fa_decode_problem;
+
+FA_API size_t fa_decode_workspace_bytes(const fa_decode_problem* prob);
+FA_API fa_status fa_decode(const fa_decode_problem* prob, const void* q, const int64_t* sq,
+                           const void* k_prefix, const int64_t* skp, const void* v_prefix,
+                           const int64_t* svp, const void* k, const int64_t* sk, const void* v,
+                           const int64_t* sv, void* o, const int64_t* so, float* lse,
+                           float* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
  * Synchronises `stream`, then reads and clears the device status word of the
  * current device.  Returns FA_OK, FA_ERR_TIMEOUT if a kernel's bounded wait on
  * an mbarrier ran out since the last call (that kernel's outputs are then
