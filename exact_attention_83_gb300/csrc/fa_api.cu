@@ -206,9 +206,10 @@ fa_status check_problem(const fa_problem* pr, Problem* out) {
 
 fa_status run_fwd(const Problem& pb, const void* q, const int64_t* sq, const void* k,
                   const int64_t* sk, const void* v, const int64_t* sv, void* o,
-                  const int64_t* so, float* lse, cudaStream_t stream) {
+                  const int64_t* so, float* lse, cudaStream_t stream, const Prefix* pfx = nullptr) {
   FwdParams p{};
   const Geo& g = pb.g;
+  if (pfx) p.pfx = *pfx;
   FA_TRY(check_tensor(q, sq, g.Bt, g.Hq, g.rows_q, pb.dtype, p.sq));
   FA_TRY(check_tensor(k, sk, g.Bt, g.Hkv, g.rows_k, pb.dtype, p.sk));
   FA_TRY(check_tensor(v, sv, g.Bt, g.Hkv, g.rows_k, pb.dtype, p.sv));
@@ -467,6 +468,79 @@ fa_status fa_bwd_ex(const fa_problem* prob, const void* q, const int64_t* sq, co
   FA_TRY(check_problem(prob, &pb));
   return run_bwd(pb, q, sq, k, sk, v, sv, dout, sdo, lse, delta, dq, sdq, dk, sdk, dv, sdv,
                  stream);
+}
+
+// The problem and the prefix of a prefix entry point.
+static fa_status check_prefix(const fa_problem* prob, int64_t P, const void* kp, const int64_t* skp,
+                              const void* vp, const int64_t* svp, Problem* pb, Prefix* pfx) {
+  FA_TRY(check_problem(prob, pb));
+  if (!pb->g.cu_q) return FA_ERR_SHAPE;             // packed sequences only
+  if (pb->drop.on) return FA_ERR_ARG;
+  const int64_t row_max = (int64_t)INT32_MAX - 1024;
+  int64_t t;
+  if (P < 0 || P > row_max || !mul_ok(pb->g.Hkv, P, &t) || !mul_ok(t, pb->D * 8, &t))
+    return FA_ERR_SHAPE;
+  // tiles of both key sets are counted in one int, rows in int32
+  if (P + pb->g.Nk > row_max) return FA_ERR_SHAPE;
+  *pfx = Prefix{};
+  pfx->on = true;
+  pfx->P = P;
+  if (P > 0) {
+    pfx->k = kp; pfx->v = vp;
+    FA_TRY(check_dense(kp, skp, 1, pb->g.Hkv, P, pb->dtype, pfx->sk));
+    FA_TRY(check_dense(vp, svp, 1, pb->g.Hkv, P, pb->dtype, pfx->sv));
+  }
+  return FA_OK;
+}
+
+fa_status fa_fwd_prefix(const fa_problem* prob, int64_t P, const void* q, const int64_t* sq,
+                        const void* k_prefix, const int64_t* skp, const void* v_prefix,
+                        const int64_t* svp, const void* k, const int64_t* sk, const void* v,
+                        const int64_t* sv, void* o, const int64_t* so, float* lse,
+                        cudaStream_t stream) {
+  Problem pb{};
+  Prefix pfx{};
+  FA_TRY(check_prefix(prob, P, k_prefix, skp, v_prefix, svp, &pb, &pfx));
+  int64_t st[4];
+  const Geo& g = pb.g;
+  FA_TRY(check_dense(q, sq, 1, g.Hq, g.rows_q, pb.dtype, st));
+  FA_TRY(check_dense(k, sk, 1, g.Hkv, g.rows_k, pb.dtype, st));
+  FA_TRY(check_dense(v, sv, 1, g.Hkv, g.rows_k, pb.dtype, st));
+  FA_TRY(check_dense(o, so, 1, g.Hq, g.rows_q, pb.dtype, st));
+  return run_fwd(pb, q, sq, k, sk, v, sv, o, so, lse, stream, &pfx);
+}
+
+fa_status fa_bwd_prefix(const fa_problem* prob, int64_t P, const void* q, const int64_t* sq,
+                        const void* k_prefix, const int64_t* skp, const void* v_prefix,
+                        const int64_t* svp, const void* k, const int64_t* sk, const void* v,
+                        const int64_t* sv, const void* dout, const int64_t* sdo, const float* lse,
+                        const float* delta, void* dq, const int64_t* sdq, void* dk_prefix,
+                        const int64_t* sdkp, void* dv_prefix, const int64_t* sdvp, void* dk,
+                        const int64_t* sdk, void* dv, const int64_t* sdv, cudaStream_t stream) {
+  Problem pb{};
+  BwdParams p{};
+  Prefix pfx{};
+  FA_TRY(check_prefix(prob, P, k_prefix, skp, v_prefix, svp, &pb, &pfx));
+  const Geo& g = pb.g;
+  int64_t st[4];
+  FA_TRY(check_dense(q, sq, 1, g.Hq, g.rows_q, pb.dtype, st));
+  FA_TRY(check_dense(dout, sdo, 1, g.Hq, g.rows_q, pb.dtype, st));
+  FA_TRY(check_dense(dq, sdq, 1, g.Hq, g.rows_q, pb.dtype, st));
+  const void* own[4] = {k, v, dk, dv};
+  const int64_t* sown[4] = {sk, sv, sdk, sdv};
+  for (int i = 0; i < 4; ++i) FA_TRY(check_dense(own[i], sown[i], 1, g.Hkv, g.rows_k, pb.dtype, st));
+  int64_t sdkp4[4] = {}, sdvp4[4] = {};
+  if (P > 0) {
+    FA_TRY(check_dense(dk_prefix, sdkp, 1, g.Hkv, P, pb.dtype, sdkp4));
+    FA_TRY(check_dense(dv_prefix, sdvp, 1, g.Hkv, P, pb.dtype, sdvp4));
+  }
+  FA_TRY(prepare_bwd(pb, q, sq, k, sk, v, sv, dout, sdo, lse, delta, dq, sdq, dk, sdk, dv, sdv, &p));
+  p.pfx = pfx;
+  p.dkp = dk_prefix; p.dvp = dv_prefix;
+  for (int i = 0; i < 4; ++i) { p.sdkp[i] = sdkp4[i]; p.sdvp[i] = sdvp4[i]; }
+  p.prof = nullptr;
+  if (use_tc(pb.dtype) && have_bwd_tc(pb.D, pb.dtype)) return launch_bwd_tc(p, stream);
+  return launch_bwd_ffma(p, stream);
 }
 
 size_t fa_dropout_mask_bytes(const fa_problem* prob) {

@@ -110,7 +110,10 @@ struct DkdvCfg : BwdShape<D> {
   static constexpr uint32_t COL_ST = 0, COL_DPT = 128, COL_DV = 256, COL_DK = 256 + D;
 };
 
-template <typename T, int D, int DROP>
+// ZR (the prefix entry points): the rows of a head's last query tile past the
+// sequence take part in no sum, whatever they hold: their weights are set to
+// 0 and their Q and dO rows are zeroed before the products that read them.
+template <typename T, int D, int DROP, bool ZR>
 __global__ void __launch_bounds__(320, 1)
     bwd_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                        const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmdo,
@@ -478,6 +481,22 @@ __global__ void __launch_bounds__(320, 1)
         for (int q = 0; q < 64; ++q)
           if (64 * hf + q < row) p[q] = 0.f;
       }
+      const int64_t qleft = Nq - static_cast<int64_t>(i) * C::BT;   // queries from this tile on
+      if constexpr (ZR) {
+        if (qleft < C::BT) {
+#pragma unroll
+          for (int q = 0; q < 64; ++q)
+            if (64 * hf + q >= qleft) p[q] = 0.f;
+          // S^T of this step is complete, so its Q tile has landed; the wait
+          // makes it visible to this thread.  dO's was waited for above.
+          const int qs = it % C::NQ;
+          if (!(ok = wait_warp(b_qfull0 + 8 * qs, (it / C::NQ) & 1, ctl, a.status, a.timeout_ns)))
+            break;
+          if (row >= qleft)
+            zero_tile_row(smem_u32(hf == 0 ? sD + ds * C::DSLOT : sQ + qs * C::TILE), row, C::DC);
+          fence_async_smem();            // published by the arrivals below
+        }
+      }
       if constexpr (DROP) {
         // P o keep, rounded pairs formed straight from p (no fp32 copy
         // kept); Z's 1 / (1 - p) scales dV when it is stored
@@ -551,6 +570,13 @@ __global__ void __launch_bounds__(320, 1)
           a23 = mul_f32x2(a23, f32x2(p[q + 2], p[q + 3]));
           f32x2_split(a01, dp[q], dp[q + 1]);
           f32x2_split(a23, dp[q + 2], dp[q + 3]);
+        }
+        if constexpr (ZR) {
+          if (qleft < C::BT) {
+#pragma unroll
+            for (int q = 0; q < 64; ++q)
+              if (64 * hf + q >= qleft) dp[q] = 0.f;
+          }
         }
         tmem_st_packed64<T>(lane_base + C::COL_DPT + 64 * hf, dp);
       }
@@ -1186,11 +1212,13 @@ __device__ __forceinline__ void tile_row_to_tmem(const uint8_t* tile, int row, u
   }
 }
 
-template <typename T, int D, int DROP>
+// PFX: the tiles of a shared prefix come before the own key tiles; the rows of
+// the last own K tile past the sequence are zeroed before the dQ product.
+template <typename T, int D, int DROP, bool PFX>
 __global__ void __launch_bounds__(320, 1)
     bwd_dq_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                      const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmdo,
-                     const BwdTcArgs a) {
+                     const BwdTcArgs a, const __grid_constant__ PrefixMaps<PFX> px) {
   using C = DqCfg<D>;
   // At D <= 64, Q and dO stay in shared memory (their stage is not reused)
   // and S, dP read them from there: no per-CTA copy into TMEM before the
@@ -1236,7 +1264,9 @@ __global__ void __launch_bounds__(320, 1)
   const int32_t hq = static_cast<int32_t>(h), hk = static_cast<int32_t>(h / a.g.G);
   const int32_t bb = static_cast<int32_t>(sv.b);
   const int nk = static_cast<int>((Nk + C::BT - 1) / C::BT);
-  const int n = a.causal ? min(static_cast<int>(qt) + 1, nk) : nk;   // key tiles to visit
+  int np = 0;                                   // prefix tiles, before the own ones
+  if constexpr (PFX) np = px.tiles;
+  const int n = np + (a.causal ? min(static_cast<int>(qt) + 1, nk) : nk);   // key tiles to visit
   if (n == 0) {
     // No key at all (an empty key sequence): dQ = 0.
     if (warp < 4) {
@@ -1256,10 +1286,14 @@ __global__ void __launch_bounds__(320, 1)
   auto load_kv = [&](int jt, int st) {
     uint8_t* stage = sStage + st * C::STAGE;
     mbar_arrive_expect_tx(b_kvfull0 + 8 * st, 2 * C::TILE);
+    const CUtensorMap *mk = &tmk, *mv = &tmv;
+    int32_t krow = static_cast<int32_t>(sv.k0 + static_cast<int64_t>(jt - np) * C::BT);
+    if constexpr (PFX) {
+      if (jt < np) { mk = &px.k; mv = &px.v; krow = jt * C::BT; }
+    }
     for (int c = 0; c < C::DC; ++c) {
-      const int32_t krow = static_cast<int32_t>(sv.k0 + static_cast<int64_t>(jt) * C::BT);
-      tma_load_4d(smem_u32(stage + c * C::CHUNK), &tmk, b_kvfull0 + 8 * st, c * 64, krow, hk, bb);
-      tma_load_4d(smem_u32(stage + C::TILE + c * C::CHUNK), &tmv, b_kvfull0 + 8 * st, c * 64,
+      tma_load_4d(smem_u32(stage + c * C::CHUNK), mk, b_kvfull0 + 8 * st, c * 64, krow, hk, bb);
+      tma_load_4d(smem_u32(stage + C::TILE + c * C::CHUNK), mv, b_kvfull0 + 8 * st, c * 64,
                   krow, hk, bb);
     }
   };
@@ -1468,8 +1502,21 @@ __global__ void __launch_bounds__(320, 1)
       mbar_arrive(b_sfree);                  // S may be overwritten by the next tile
       // keys past N (last tile) and keys after the query (diagonal tile)
       int lim = 63;
-      if (a.causal && jt == qt) lim = row - 64 * hf;
-      if (jt == nk - 1) lim = min(lim, static_cast<int>(Nk - 1 - static_cast<int64_t>(jt) * C::BT) - 64 * hf);
+      if (a.causal && jt - np == qt) lim = row - 64 * hf;
+      if (jt == np + nk - 1)
+        lim = min(lim, static_cast<int>(Nk - 1 - static_cast<int64_t>(jt - np) * C::BT) - 64 * hf);
+      if constexpr (PFX) {
+        if (jt < np) lim = jt == np - 1 ? px.lim_last - 64 * hf : 63;
+        const int64_t kleft = Nk - static_cast<int64_t>(jt - np) * C::BT;   // own keys from here on
+        if (jt >= np && kleft < C::BT) {
+          const int st = jt % NR;
+          if (!(ok = wait_warp(b_kvfull0 + 8 * st, (jt / NR) & 1, ctl, a.status, a.timeout_ns))) break;
+          // each warpgroup zeroes one chunk of the rows (one has them all at D <= 64)
+          if (row >= kleft && hf < C::DC)
+            zero_tile_row(smem_u32(sStage + st * C::STAGE + hf * C::CHUNK), row, 1);
+          fence_async_smem();            // published by the dS-ready arrival below
+        }
+      }
       {
         // P = exp2(c * S - L * log2(e)), two keys per paired instruction
         const uint64_t cc = f32x2(c, c), nl = f32x2(-l2, -l2);
@@ -1526,6 +1573,13 @@ __global__ void __launch_bounds__(320, 1)
         for (int q = 0; q < 64; q += 2) {
           const uint64_t x = mul_f32x2(add_f32x2(f32x2(dp[q], dp[q + 1]), nd), f32x2(p[q], p[q + 1]));
           f32x2_split(x, dp[q], dp[q + 1]);
+        }
+        if constexpr (PFX) {
+          if (lim < 63) {
+#pragma unroll
+            for (int q = 0; q < 64; ++q)
+              if (q > lim) dp[q] = 0.f;
+          }
         }
         tmem_st_packed64<T>(lane_base + C::COL_DP + 64 * hf, dp);
       }
@@ -1640,7 +1694,7 @@ fa_status run_bwd_tc(const BwdParams& p, cudaStream_t stream) {
   bool persist = false;
   if constexpr (D == 64 && DROP == kDropNone)
     persist = split == 1 && g.Nq <= kPersistMaxN && g.Nk <= kPersistMaxN;
-  auto k1 = bwd_dkdv_tc_kernel<T, D, DROP>;
+  auto k1 = bwd_dkdv_tc_kernel<T, D, DROP, false>;
   if (persist) {
     auto kp = bwd_dkdv_persist_kernel<T>;
     if (cudaFuncSetAttribute(kp, cudaFuncAttributeMaxDynamicSharedMemorySize, DkdvPCfg::SMEM) !=
@@ -1689,11 +1743,11 @@ fa_status run_bwd_tc(const BwdParams& p, cudaStream_t stream) {
   if (blocks2 > 0x7fffffffLL) return FA_ERR_SHAPE;
   a.out0 = p.dq; a.out1 = nullptr;
   for (int i = 0; i < 4; ++i) { a.s0[i] = p.sdq[i]; a.s1[i] = 0; }
-  auto k2 = bwd_dq_tc_kernel<T, D, DROP>;
+  auto k2 = bwd_dq_tc_kernel<T, D, DROP, false>;
   if (cudaFuncSetAttribute(k2, cudaFuncAttributeMaxDynamicSharedMemorySize, DqCfg<D>::SMEM) != cudaSuccess)
     return FA_ERR_LAUNCH;
   k2<<<dim3(static_cast<unsigned>(blocks2)), dim3(DqCfg<D>::THREADS), DqCfg<D>::SMEM, s2>>>(
-      mq, mk, mv, mdo, a);
+      mq, mk, mv, mdo, a, PrefixMaps<false>{});
   if (cudaGetLastError() != cudaSuccess) return FA_ERR_LAUNCH;
   if (concurrent) {
     const fa_status st = join.end();
@@ -1703,8 +1757,102 @@ fa_status run_bwd_tc(const BwdParams& p, cudaStream_t stream) {
   return FA_OK;
 }
 
+// dK / dV of one set of keys (`g`: the sequences' own, or the prefix against
+// all query rows) for the prefix entry points.
+template <typename T, int D>
+fa_status launch_dkdv_zr(const BwdParams& p, const Geo& g, const CUtensorMap& mq,
+                         const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mdo,
+                         BwdTcArgs a, cudaStream_t stream) {
+  a.g = g;
+  a.BH = g.B * g.Hkv; a.ntiles = (g.Nk + 127) / 128;
+  a.hgroup = head_group(a.BH, 2 * g.Nq * p.D * 2 * g.G);
+  const int64_t base = a.BH * a.ntiles;
+  int split = 1;
+  while (split < 8 && g.G % (2 * split) == 0 && base * split < 2 * device_sm_count()) split *= 2;
+  a.split = split;
+  const int64_t blocks = base * split;
+  if (blocks > 0x7fffffffLL) return FA_ERR_SHAPE;
+  auto kern = bwd_dkdv_tc_kernel<T, D, kDropNone, true>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, DkdvCfg<D>::SMEM) !=
+      cudaSuccess)
+    return FA_ERR_LAUNCH;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+  cfg.blockDim = dim3(DkdvCfg<D>::THREADS);
+  cfg.dynamicSmemBytes = DkdvCfg<D>::SMEM;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  if (split > 1) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(split);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+  }
+  if (cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, mdo, a) != cudaSuccess) return FA_ERR_LAUNCH;
+  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+}
+
+// Backward behind a shared prefix: dK / dV of the own keys, dK / dV of the
+// prefix (every packed query row against it, as one sequence), and dQ over
+// both sets of keys.  All three rebuild P from the one log-sum-exp over both.
+template <typename T, int D>
+fa_status run_bwd_prefix(const BwdParams& p, cudaStream_t stream) {
+  const Geo& g = p.g;
+  CUtensorMap mq, mk, mv, mdo;
+  PrefixMaps<true> px{};
+  if (!encode_tile_map(&mq, p.q, p.dtype, g.Bt, g.Hq, g.rows_q, p.D, p.sq, 128, 64) ||
+      !encode_tile_map(&mk, p.k, p.dtype, g.Bt, g.Hkv, g.rows_k, p.D, p.sk, 128, 64) ||
+      !encode_tile_map(&mv, p.v, p.dtype, g.Bt, g.Hkv, g.rows_k, p.D, p.sv, 128, 64) ||
+      !encode_tile_map(&mdo, p.dout, p.dtype, g.Bt, g.Hq, g.rows_q, p.D, p.sdo, 128, 64))
+    return FA_ERR_LAUNCH;
+  px.k = mk; px.v = mv;                   // never read when there is no prefix tile
+  if (p.pfx.P > 0 &&
+      (!encode_tile_map(&px.k, p.pfx.k, p.dtype, 1, g.Hkv, p.pfx.P, p.D, p.pfx.sk, 128, 64) ||
+       !encode_tile_map(&px.v, p.pfx.v, p.dtype, 1, g.Hkv, p.pfx.P, p.D, p.pfx.sv, 128, 64)))
+    return FA_ERR_LAUNCH;
+  px.tiles = static_cast<int>((p.pfx.P + 127) / 128);
+  px.lim_last = static_cast<int>((p.pfx.P + 127) % 128);
+  BwdTcArgs a{};
+  a.dreal = static_cast<int>(p.D);
+  a.lse = p.lse; a.delta = p.delta;
+  a.causal = p.causal;
+  a.c = p.scale * kLog2e;
+  a.scale = p.scale;
+  a.status = p.status;
+  a.timeout_ns = p.timeout_ns;
+  a.out0 = p.dv; a.out1 = p.dk;
+  for (int i = 0; i < 4; ++i) { a.s0[i] = p.sdv[i]; a.s1[i] = p.sdk[i]; }
+  fa_status st = launch_dkdv_zr<T, D>(p, g, mq, mk, mv, mdo, a, stream);
+  if (st != FA_OK) return st;
+  if (p.pfx.P > 0) {
+    a.causal = 0;
+    a.out0 = p.dvp; a.out1 = p.dkp;
+    for (int i = 0; i < 4; ++i) { a.s0[i] = p.sdvp[i]; a.s1[i] = p.sdkp[i]; }
+    st = launch_dkdv_zr<T, D>(p, prefix_geo(g, p.pfx.P), mq, px.k, px.v, mdo, a, stream);
+    if (st != FA_OK) return st;
+  }
+  a.g = g;
+  a.causal = p.causal;
+  a.split = 1;
+  a.BH = g.B * g.Hq; a.ntiles = (g.Nq + 127) / 128;
+  a.hgroup = head_group(a.BH, 2 * (g.Nk + p.pfx.P) * p.D * 2);
+  const int64_t blocks = a.BH * a.ntiles;
+  if (blocks > 0x7fffffffLL) return FA_ERR_SHAPE;
+  a.out0 = p.dq; a.out1 = nullptr;
+  for (int i = 0; i < 4; ++i) { a.s0[i] = p.sdq[i]; a.s1[i] = 0; }
+  auto kern = bwd_dq_tc_kernel<T, D, kDropNone, true>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, DqCfg<D>::SMEM) != cudaSuccess)
+    return FA_ERR_LAUNCH;
+  kern<<<dim3(static_cast<unsigned>(blocks)), dim3(DqCfg<D>::THREADS), DqCfg<D>::SMEM, stream>>>(
+      mq, mk, mv, mdo, a, px);
+  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+}
+
 template <typename T, int D>
 fa_status run_bwd_tc_any(const BwdParams& p, cudaStream_t s) {
+  if (p.pfx.on) return run_bwd_prefix<T, D>(p, s);
   const int dm = bwd_drop_mode(p.drop);
   return dm == kDropRead ? run_bwd_tc<T, D, kDropRead>(p, s)
          : dm == kDropDraw ? run_bwd_tc<T, D, kDropDraw>(p, s) : run_bwd_tc<T, D, kDropNone>(p, s);

@@ -44,6 +44,13 @@
 // the 16 bytes there for the backward.  P V takes P o keep; the 1 / (1 - p)
 // of Z is folded into the final 1 / l.
 //
+// Shared prefix (template flag PFX): the key tiles of a prefix that every
+// sequence sees in full come first, then the sequence's own; one running
+// maximum and sum over both, so nothing is joined or rounded in between.  The
+// prefix's last tile is zero-filled by its tensor map; the rows of a
+// sequence's last own V tile that belong to the next sequence (or to padding)
+// are zeroed before the product.
+//
 // Every mbarrier wait is bounded (see tc_common.cuh); a wait that runs out
 // records FA_ERR_TIMEOUT, the CTA drains its copies and MMAs in flight,
 // releases its tensor memory and exits.
@@ -94,10 +101,11 @@ struct FwdTcArgs {
   int withhold_arrival;    // test-only: CTA 0 skips the first S-ready arrival of tile 0
 };
 
-template <typename T, int D, int DROP>
+template <typename T, int D, int DROP, bool PFX>
 __global__ void __launch_bounds__(320, 1)
     fwd_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
-                  const __grid_constant__ CUtensorMap tmv, const FwdTcArgs a) {
+                  const __grid_constant__ CUtensorMap tmv, const FwdTcArgs a,
+                  const __grid_constant__ PrefixMaps<PFX> px) {
   using C = FwdCfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -134,12 +142,14 @@ __global__ void __launch_bounds__(320, 1)
   const int32_t hq = static_cast<int32_t>(h), hk = static_cast<int32_t>(h / a.g.G);
   const int32_t bb = static_cast<int32_t>(sv.b);
   const int nk = static_cast<int>((Nk + C::BN - 1) / C::BN);
+  int np = 0;                                   // prefix tiles, before the own ones
+  if constexpr (PFX) np = px.tiles;
   int ntile[2];
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
     const int64_t qt = 2 * pr + g;
     const int64_t diag = qt + 1;   // key tiles up to and including the diagonal
-    ntile[g] = (qt * C::BM >= Nq) ? 0 : (a.causal ? static_cast<int>(diag < nk ? diag : nk) : nk);
+    ntile[g] = (qt * C::BM >= Nq) ? 0 : np + (a.causal ? static_cast<int>(diag < nk ? diag : nk) : nk);
   }
   const int nmax = max(ntile[0], ntile[1]);
   if (nmax == 0) {
@@ -172,13 +182,19 @@ __global__ void __launch_bounds__(320, 1)
     const int s = u % C::NP;
     const bool hasV = u > 0, hasK = u < nmax;
     mbar_arrive_expect_tx(b_full0 + 8 * s, (hasV ? C::TILE : 0) + (hasK ? C::TILE : 0));
+    const CUtensorMap *mk = &tmk, *mv = &tmv;
+    int32_t rk = static_cast<int32_t>(sv.k0 + static_cast<int64_t>(u - np) * C::BN), rv = rk - C::BN;
+    if constexpr (PFX) {
+      if (u < np) { mk = &px.k; rk = u * C::BN; }
+      if (u - 1 < np) { mv = &px.v; rv = (u - 1) * C::BN; }
+    }
     for (int c = 0; c < C::DC; ++c) {
       if (hasV)
-        tma_load_4d(smem_u32(sRing + s * C::PAIR + c * C::CHUNK), &tmv, b_full0 + 8 * s, c * 64,
-                    static_cast<int32_t>(sv.k0 + (u - 1) * C::BN), hk, bb);
+        tma_load_4d(smem_u32(sRing + s * C::PAIR + c * C::CHUNK), mv, b_full0 + 8 * s, c * 64, rv,
+                    hk, bb);
       if (hasK)
-        tma_load_4d(smem_u32(sRing + s * C::PAIR + C::TILE + c * C::CHUNK), &tmk, b_full0 + 8 * s,
-                    c * 64, static_cast<int32_t>(sv.k0 + u * C::BN), hk, bb);
+        tma_load_4d(smem_u32(sRing + s * C::PAIR + C::TILE + c * C::CHUNK), mk, b_full0 + 8 * s,
+                    c * 64, rk, hk, bb);
     }
     issued[s] = static_cast<uint32_t>(u / C::NP) + 1;
   };
@@ -372,8 +388,20 @@ __global__ void __launch_bounds__(320, 1)
       // Exclude keys past N (last key tile) and keys after the query (the
       // diagonal tile, the only one a causal row can straddle).
       int lim = C::BN - 1;
-      if (a.causal && j == qt) lim = r;
-      if (j == nk - 1) lim = min(lim, lim_last);
+      if (a.causal && j - np == qt) lim = r;
+      if (j == np + nk - 1) lim = min(lim, lim_last);
+      if constexpr (PFX) {
+        if (j < np) lim = j == np - 1 ? px.lim_last : C::BN - 1;
+        if (j >= np && j == np + nk - 1 && lim_last < C::BN - 1) {
+          // V_j came with unit j + 1, the last of its slot
+          const int u = j + 1;
+          if (!(ok = wait_warp(b_full0 + 8 * (u % C::NP), (u / C::NP) & 1, ctl, a.status,
+                               a.timeout_ns)))
+            break;
+          if (r > lim_last) zero_tile_row(smem_u32(sRing + (u % C::NP) * C::PAIR), r, C::DC);
+          fence_async_smem();          // published by the P-ready arrival below
+        }
+      }
       if (lim < C::BN - 1) {
 #pragma unroll
         for (int kk = 0; kk < C::BN; ++kk)
@@ -520,10 +548,11 @@ struct Fwd1Cfg {
   static constexpr uint32_t COL_S = 0, COL_O = 128, COL_P = 192;
 };
 
-template <typename T, int DROP>
+template <typename T, int DROP, bool PFX>
 __global__ void __launch_bounds__(192, 2)
     fwd_tc_1t_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
-                     const __grid_constant__ CUtensorMap tmv, const FwdTcArgs a) {
+                     const __grid_constant__ CUtensorMap tmv, const FwdTcArgs a,
+                     const __grid_constant__ PrefixMaps<PFX> px) {
   using C = Fwd1Cfg;
   constexpr int D = C::D;
   static_assert(2 * C::SMEM <= 227 * 1024, "two CTAs per SM");
@@ -560,7 +589,9 @@ __global__ void __launch_bounds__(192, 2)
   const int32_t hq = static_cast<int32_t>(h), hk = static_cast<int32_t>(h / a.g.G);
   const int32_t bb = static_cast<int32_t>(sv.b);
   const int nk = static_cast<int>((Nk + C::BN - 1) / C::BN);
-  const int n = a.causal ? min(static_cast<int>(qt) + 1, nk) : nk;   // key tiles to visit
+  int np = 0;                                   // prefix tiles, before the own ones
+  if constexpr (PFX) np = px.tiles;
+  const int n = np + (a.causal ? min(static_cast<int>(qt) + 1, nk) : nk);   // key tiles to visit
   if (n == 0) {
     // No key at all (an empty key sequence): O = 0 and L = -inf.
     if (warp < 4) {
@@ -589,8 +620,12 @@ __global__ void __launch_bounds__(192, 2)
     if (j >= n) return;
     const int s = u % C::NS;
     mbar_arrive_expect_tx(b_full0 + 8 * s, C::TILE);
-    tma_load_4d(smem_u32(sRing + s * C::TILE), kv ? &tmv : &tmk, b_full0 + 8 * s, 0,
-                static_cast<int32_t>(sv.k0 + j * C::BN), hk, bb);
+    const CUtensorMap* map = kv ? &tmv : &tmk;
+    int32_t row = static_cast<int32_t>(sv.k0 + static_cast<int64_t>(j - np) * C::BN);
+    if constexpr (PFX) {
+      if (j < np) { map = kv ? &px.v : &px.k; row = j * C::BN; }
+    }
+    tma_load_4d(smem_u32(sRing + s * C::TILE), map, b_full0 + 8 * s, 0, row, hk, bb);
     issued[s] = static_cast<uint32_t>(u / C::NS) + 1;
   };
   const int u_early = 2 * n + 1 < C::NS ? 2 * n + 1 : C::NS;   // round 0 of the ring
@@ -759,8 +794,19 @@ __global__ void __launch_bounds__(192, 2)
       // Exclude keys past the sequence (last key tile) and keys after the
       // query (the diagonal tile, the only one a causal row can straddle).
       int lim = C::BN - 1;
-      if (a.causal && j == qt) lim = r;
-      if (j == nk - 1) lim = min(lim, lim_last);
+      if (a.causal && j - np == qt) lim = r;
+      if (j == np + nk - 1) lim = min(lim, lim_last);
+      if constexpr (PFX) {
+        if (j < np) lim = j == np - 1 ? px.lim_last : C::BN - 1;
+        if (j >= np && j == np + nk - 1 && lim_last < C::BN - 1) {
+          const int uv = unit_v(j);    // the last unit of its slot
+          if (!(ok = wait_warp(b_full0 + 8 * (uv % C::NS), (uv / C::NS) & 1, ctl, a.status,
+                               a.timeout_ns)))
+            break;
+          if (r > lim_last) zero_tile_row(smem_u32(sRing + (uv % C::NS) * C::TILE), r, 1);
+          fence_async_smem();          // published by the P-ready arrival below
+        }
+      }
       if (lim < C::BN - 1) {
 #pragma unroll
         for (int kk = 0; kk < C::BN; ++kk)
@@ -876,7 +922,7 @@ __global__ void __launch_bounds__(192, 2)
   }
 }
 
-template <typename T, int D>
+template <typename T, int D, int DROP, bool PFX>
 fa_status run_fwd_tc(const FwdParams& p, cudaStream_t stream) {
   using C = FwdCfg<D>;
   const Geo& g = p.g;
@@ -893,7 +939,7 @@ fa_status run_fwd_tc(const FwdParams& p, cudaStream_t stream) {
   a.g = g;
   a.BH = g.B * g.Hq; a.npairs = (g.Nq + 255) / 256;
   // K and V of a head: the operand all of its CTAs read
-  a.hgroup = head_group(a.BH, 2 * g.Nk * p.D * (p.dtype == FA_F32 ? 4 : 2));
+  a.hgroup = head_group(a.BH, 2 * (g.Nk + p.pfx.P) * p.D * (p.dtype == FA_F32 ? 4 : 2));
   for (int i = 0; i < 4; ++i) a.so[i] = p.so[i];
   a.causal = p.causal;
   a.c = p.scale * kLog2e;
@@ -901,6 +947,16 @@ fa_status run_fwd_tc(const FwdParams& p, cudaStream_t stream) {
   a.status = p.status;
   a.timeout_ns = p.timeout_ns;
   a.withhold_arrival = p.withhold_arrival;
+  PrefixMaps<PFX> px{};
+  if constexpr (PFX) {
+    px.k = mk; px.v = mv;                 // never read when there is no prefix tile
+    if (p.pfx.P > 0 &&
+        (!encode_tile_map(&px.k, p.pfx.k, p.dtype, 1, g.Hkv, p.pfx.P, p.D, p.pfx.sk, 128, 64) ||
+         !encode_tile_map(&px.v, p.pfx.v, p.dtype, 1, g.Hkv, p.pfx.P, p.D, p.pfx.sv, 128, 64)))
+      return FA_ERR_LAUNCH;
+    px.tiles = static_cast<int>((p.pfx.P + 127) / 128);
+    px.lim_last = static_cast<int>((p.pfx.P + 127) % 128);
+  }
   const int64_t blocks = a.BH * a.npairs;
   if (blocks > 0x7fffffffLL) return FA_ERR_SHAPE;
   if constexpr (D == 64) {
@@ -908,20 +964,28 @@ fa_status run_fwd_tc(const FwdParams& p, cudaStream_t stream) {
     a.npairs = (g.Nq + 127) / 128;
     const int64_t blocks1 = a.BH * a.npairs;
     if (blocks1 > 0x7fffffffLL) return FA_ERR_SHAPE;
-    auto kern = p.drop.on ? fwd_tc_1t_kernel<T, kDropDraw> : fwd_tc_1t_kernel<T, kDropNone>;
+    auto kern = fwd_tc_1t_kernel<T, DROP, PFX>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Fwd1Cfg::SMEM) !=
         cudaSuccess)
       return FA_ERR_LAUNCH;
     kern<<<dim3(static_cast<unsigned>(blocks1)), dim3(Fwd1Cfg::THREADS), Fwd1Cfg::SMEM, stream>>>(
-        mq, mk, mv, a);
+        mq, mk, mv, a, px);
   } else {
-    auto kern = p.drop.on ? fwd_tc_kernel<T, D, kDropDraw> : fwd_tc_kernel<T, D, kDropNone>;
+    auto kern = fwd_tc_kernel<T, D, DROP, PFX>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
         cudaSuccess)
       return FA_ERR_LAUNCH;
-    kern<<<dim3(static_cast<unsigned>(blocks)), dim3(C::THREADS), C::SMEM, stream>>>(mq, mk, mv, a);
+    kern<<<dim3(static_cast<unsigned>(blocks)), dim3(C::THREADS), C::SMEM, stream>>>(mq, mk, mv, a,
+                                                                                              px);
   }
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+}
+
+template <typename T, int D>
+fa_status run_fwd_tc_any(const FwdParams& p, cudaStream_t s) {
+  if (p.pfx.on) return run_fwd_tc<T, D, kDropNone, true>(p, s);
+  return p.drop.on ? run_fwd_tc<T, D, kDropDraw, false>(p, s)
+                   : run_fwd_tc<T, D, kDropNone, false>(p, s);
 }
 
 }  // namespace
@@ -933,11 +997,11 @@ bool have_fwd_tc(int64_t D, fa_dtype dt) {
 
 fa_status launch_fwd_tc(const FwdParams& p, cudaStream_t s) {
   if (p.dtype == FA_BF16) {
-    if (p.D == 128) return run_fwd_tc<__nv_bfloat16, 128>(p, s);
-    if (p.D <= 64) return run_fwd_tc<__nv_bfloat16, 64>(p, s);
+    if (p.D == 128) return run_fwd_tc_any<__nv_bfloat16, 128>(p, s);
+    if (p.D <= 64) return run_fwd_tc_any<__nv_bfloat16, 64>(p, s);
   } else if (p.dtype == FA_F16) {
-    if (p.D == 128) return run_fwd_tc<__half, 128>(p, s);
-    if (p.D <= 64) return run_fwd_tc<__half, 64>(p, s);
+    if (p.D == 128) return run_fwd_tc_any<__half, 128>(p, s);
+    if (p.D <= 64) return run_fwd_tc_any<__half, 64>(p, s);
   }
   return FA_ERR_ARG;
 }

@@ -21,7 +21,8 @@ struct Geo {
   int64_t B, Hq, Hkv, G;     // G = Hq / Hkv
   int64_t Nq, Nk;            // rows per sequence (upper bounds when packed)
   const int32_t* cu_q;       // device, B+1 entries, or null (fixed lengths)
-  const int32_t* cu_k;
+  const int32_t* cu_k;       // packed queries without it: one run of Nk keys
+  int64_t joined;            // further sequences whose query rows join this one's (0)
   int64_t rows_q, rows_k;    // tensor rows per (b, h): Nq, Nk, or the packed totals
   int64_t Bt;                // batch extent of the tensors: B, or 1 when packed
 };
@@ -49,6 +50,15 @@ struct Dropout {
   int64_t mask_kt;
 };
 
+// Keys and values in front of every sequence's own (fa_fwd_prefix): P rows of
+// Hkv heads that all sequences see in full.  P = 0: none.
+struct Prefix {
+  const void* k; const void* v;
+  int64_t P;
+  int64_t sk[4], sv[4];
+  bool on;                   // the call is one of the prefix entry points
+};
+
 // Parameters of one forward call.
 struct FwdParams {
   const void* q; const void* k; const void* v;
@@ -63,6 +73,7 @@ struct FwdParams {
   unsigned int* status;   // device status word (first error a kernel records)
   uint64_t timeout_ns;    // bound on any single device-side wait
   int withhold_arrival;   // test-only: CTA 0 skips one mbarrier arrival (see fa.h)
+  Prefix pfx;
 };
 
 struct PreParams {
@@ -88,7 +99,22 @@ struct BwdParams {
   const cudaEvent_t* prof;   // 3 events to record around the two kernels, or null
   int withhold_arrival;      // test-only (single-pass backward): see fa.h
   bool allow_side;           // the dQ kernel may run on the device's side stream
+  Prefix pfx;
+  void* dkp; void* dvp;      // gradients of the prefix (pfx.on)
+  int64_t sdkp[4], sdvp[4];
 };
+
+// The geometry of the prefix's dK / dV: all packed query rows against the
+// prefix keys, as one sequence.
+inline Geo prefix_geo(const Geo& g, int64_t P) {
+  Geo r = g;
+  r.joined = g.B - 1;
+  r.B = 1;
+  r.Nq = g.rows_q;
+  r.Nk = r.rows_k = P;
+  r.cu_k = nullptr;
+  return r;
+}
 
 #ifdef __CUDACC__
 // One sequence as a kernel sees it: batch coordinate of the tensors, first
@@ -106,8 +132,8 @@ __device__ __forceinline__ SeqView seq_view(const Geo& g, int64_t b) {
     v.b = b; v.q0 = 0; v.k0 = 0; v.nq = g.Nq; v.nk = g.Nk; v.ok = true;
     return v;
   }
-  const int64_t q0 = __ldg(g.cu_q + b), q1 = __ldg(g.cu_q + b + 1);
-  const int64_t k0 = __ldg(g.cu_k + b), k1 = __ldg(g.cu_k + b + 1);
+  const int64_t q0 = __ldg(g.cu_q + b), q1 = __ldg(g.cu_q + b + 1 + g.joined);
+  const int64_t k0 = g.cu_k ? __ldg(g.cu_k + b) : 0, k1 = g.cu_k ? __ldg(g.cu_k + b + 1) : g.Nk;
   v.b = 0; v.q0 = q0; v.k0 = k0; v.nq = q1 - q0; v.nk = k1 - k0;
   v.ok = q0 >= 0 && q1 >= q0 && q1 <= g.rows_q && v.nq <= g.Nq &&
          k0 >= 0 && k1 >= k0 && k1 <= g.rows_k && v.nk <= g.Nk;

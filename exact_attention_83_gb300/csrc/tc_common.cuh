@@ -321,6 +321,30 @@ constexpr uint32_t idesc_f16(int M, int N, bool a_mn_major, bool b_mn_major) {
          ((static_cast<uint32_t>(M) >> 4) << 24);
 }
 
+// ---------------------------------------------------------------- shared prefix
+// Tensor maps of a prefix in front of every sequence's own keys (kernel
+// template flag PFX); an empty parameter without one.
+template <bool PFX>
+struct PrefixMaps {};
+template <>
+struct PrefixMaps<true> {
+  CUtensorMap k, v;
+  int tiles;       // key tiles of 128
+  int lim_last;    // last valid key of the last one
+};
+
+// Zeroes row `row` of a 128-byte-swizzled tile of `chunks` chunks
+// (64-column chunks of 128 rows x 128 bytes): the rows of an operand tile past
+// the sequence, whose weights are 0, may hold anything, and 0 times an
+// infinity or NaN would reach the sums.  The caller fences before it releases
+// the tile to the tensor cores.
+__device__ __forceinline__ void zero_tile_row(uint32_t tile, int row, int chunks) {
+  for (int c = 0; c < chunks; ++c)
+#pragma unroll
+    for (int u = 0; u < 8; ++u)
+      st_shared_v4(tile + static_cast<uint32_t>(c * 16384 + row * 128 + u * 16), 0u, 0u, 0u, 0u);
+}
+
 // ---------------------------------------------------------------- packing
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(float lo, float hi);

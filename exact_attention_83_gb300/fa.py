@@ -47,8 +47,17 @@ RMS norm of every head in the same pass (fa_rotary_fwd / fa_rotary_bwd):
   rotary_fwd / rotary_bwd, qk_norm_rotary_fwd / qk_norm_rotary_bwd: the same with
                                     outputs allocated (or given as out=)
   Rotary(...)                       the same choices as one value, which
-                                    attention_gqa(..., rotary=) and
-                                    attention_varlen(..., rotary=) apply first
+                                    attention_gqa(..., rotary=),
+                                    attention_varlen(..., rotary=) and
+                                    attention_varlen_prefix(..., rotary=) apply first
+
+Packed sequences behind one shared prefix (fa_fwd_prefix / fa_bwd_prefix): every
+query sees the whole prefix and its own sequence's keys:
+  attention_varlen_prefix(q, k, v, k_prefix, v_prefix, cu_seqlens_q, cu_seqlens_k,
+                          max_seqlen_q, max_seqlen_k, causal, scale, rotary)
+                                    -> o with autograd, also for the prefix
+  attention_prefix_fwd / attention_prefix_bwd: the same with outputs allocated
+  fwd_prefix / bwd_prefix           write the tensors given
 
 Serving (fa_decode): the newest tokens of a batch whose keys are a prefix that
 all requests share, followed by each request's own cache rows:
@@ -65,8 +74,10 @@ cu_seqlens_* int32 CUDA tensors of B+1 offsets, max_seqlen_* host ints.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
+import struct
 import threading
 from typing import NamedTuple, Optional, Sequence
 
@@ -93,7 +104,7 @@ EXPORTED = ("fa_fwd", "fa_bwd_preprocess", "fa_bwd", "fa_get_device_status",
             "fa_bwd_fused_workspace_bytes", "fa_bwd_fused", "fa_dropout_mask_bytes",
             "fa_dropout_mask", "fa_test_set_l2_bytes", "fa_rotary_fwd",
             "fa_rotary_bwd_workspace_bytes", "fa_rotary_bwd", "fa_decode_workspace_bytes",
-            "fa_decode")
+            "fa_decode", "fa_fwd_prefix", "fa_bwd_prefix")
 
 
 class Problem(ctypes.Structure):
@@ -143,6 +154,8 @@ _s4 = ctypes.POINTER(ctypes.c_int64)
 def load_library(path: str = LIB_PATH):
     """Load libfa.so and declare its signatures.  Raises if it is missing."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -181,19 +194,20 @@ def load_library(path: str = LIB_PATH):
         lib.fa_dropout_mask_bytes.restype = ctypes.c_size_t
         lib.fa_dropout_mask.argtypes = [_pp, _vp, ctypes.c_size_t, _vp]
         lib.fa_dropout_mask.restype = ctypes.c_int
-        _pr = ctypes.POINTER(RotaryProblem)
-        lib.fa_rotary_fwd.argtypes = [_pr, _vp, _s4, _vp, _s4, _vp, _s4, _vp, _s4, _vp]
+        # structs and strides as plain addresses: ctypes objects and packed bytes pass
+        lib.fa_rotary_fwd.argtypes = [_vp] * 10
         lib.fa_rotary_fwd.restype = ctypes.c_int
-        lib.fa_rotary_bwd_workspace_bytes.argtypes = [_pr]
+        lib.fa_rotary_bwd_workspace_bytes.argtypes = [_vp]
         lib.fa_rotary_bwd_workspace_bytes.restype = ctypes.c_size_t
-        lib.fa_rotary_bwd.argtypes = [_pr, _vp, _s4, _vp, _s4, _vp, _s4, _vp, _s4, _vp, _s4, _vp,
-                                      _s4, _vp, _vp, _vp, ctypes.c_size_t, _vp]
+        lib.fa_rotary_bwd.argtypes = [_vp] * 16 + [ctypes.c_size_t, _vp]
         lib.fa_rotary_bwd.restype = ctypes.c_int
-        _pd = ctypes.POINTER(DecodeProblem)
-        lib.fa_decode_workspace_bytes.argtypes = [_pd]
+        lib.fa_fwd_prefix.argtypes = [_vp, _i64] + [_vp] * 14
+        lib.fa_fwd_prefix.restype = ctypes.c_int
+        lib.fa_bwd_prefix.argtypes = [_vp, _i64] + [_vp] * 25
+        lib.fa_bwd_prefix.restype = ctypes.c_int
+        lib.fa_decode_workspace_bytes.argtypes = [_vp]
         lib.fa_decode_workspace_bytes.restype = ctypes.c_size_t
-        lib.fa_decode.argtypes = [_pd, _vp, _s4, _vp, _s4, _vp, _s4, _vp, _s4, _vp, _s4, _vp, _s4,
-                                  _vp, _vp, ctypes.c_size_t, _vp]
+        lib.fa_decode.argtypes = [_vp] * 15 + [ctypes.c_size_t, _vp]
         lib.fa_decode.restype = ctypes.c_int
         lib.fa_get_device_status.argtypes = [_vp]
         lib.fa_get_device_status.restype = ctypes.c_int
@@ -403,62 +417,93 @@ class Rotary(NamedTuple):
     eps: float = 1e-6
 
 
-def _rotary_problem(q, k, rot: Rotary):
-    """struct fa_rotary of a call, and whether the tensors are packed."""
-    if q.dtype not in _DTYPE_CODE or not q.is_cuda:
+# The calls below run once per layer and token in serving, where their host
+# time is what a step waits for: strides and structs are packed straight into
+# bytes (the C layouts of int64[4], fa_rotary, fa_decode_problem and fa_problem) instead of
+# through ctypes objects and views, and the device is only switched when it is
+# not the current one.
+_PACK4 = struct.Struct("@4q").pack
+_PACK_ROTARY = struct.Struct("@5q2iq4qPP3q2iPPf0q").pack
+_PACK_DECODE = struct.Struct("@7qPifi0q").pack
+_PACK_PROBLEM = struct.Struct("@6qPP2qififQIP").pack
+
+
+def _call(fn, where: str, dev: int, *args):
+    """fn(*args, stream) with the current stream of device `dev`."""
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    if torch._C._cuda_getDevice() == dev:
+        code = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            code = fn(*args, stream)
+    if code != 0:
+        raise FAError(code, where)
+
+
+def _strides4(t: torch.Tensor) -> bytes:
+    """int64[4] strides (b, h, n, d) of [B, H, N, D] or packed [N, H, D]."""
+    st = t.stride()
+    return _PACK4(*st) if len(st) == 4 else _PACK4(0, st[1], st[0], st[2])
+
+
+def _rotary_problem(q, k, rot: Rotary) -> bytes:
+    """struct fa_rotary of a call."""
+    dt = q.dtype
+    if dt not in _DTYPE_CODE or not q.is_cuda:
         raise TypeError("tensors must be CUDA float32, float16 or bfloat16")
-    if q.dim() not in (3, 4) or k.dim() != q.dim():
+    dev = q.get_device()
+    qs, ks = q.shape, k.shape
+    if len(qs) == 4:
+        B, Hq, N, D = qs
+        packed = False
+    elif len(qs) == 3:
+        N, Hq, D = qs
+        B, packed = 1, True
+    else:
         raise ValueError("expected [B, H, N, D] or packed [T, H, D] tensors")
-    if k.dtype != q.dtype or k.device != q.device or k.shape[-1] != q.shape[-1]:
-        raise ValueError("q and k must share dtype, device and head dimension")
-    packed = q.dim() == 3
-    q4, k4 = _as4(q, packed), _as4(k, packed)
-    B, Hq, N, D = q4.shape
-    if k4.shape[0] != B or k4.shape[2] != N:
+    if k.dtype != dt or k.get_device() != dev or len(ks) != len(qs) or ks[-1] != D:
+        raise ValueError("q and k must share dtype, device, layout and head dimension")
+    Hkv = ks[1]
+    if (ks[0] != N) if packed else (ks[0] != B or ks[2] != N):
         raise ValueError("q and k must share batch and length")
-    pos, freq = rot.positions, rot.inv_freq
-    if freq.dtype != torch.float32 or freq.device != q.device or freq.dim() != 1 \
+    pos, freq, sections, interleaved, qw, kw, eps = rot
+    pairs = freq.numel()
+    if freq.dtype != torch.float32 or freq.get_device() != dev or freq.dim() != 1 \
             or not freq.is_contiguous():
         raise ValueError("inv_freq: a contiguous float32 vector on q's device")
-    if pos.dtype not in (torch.int32, torch.int64) or pos.device != q.device:
+    pos64 = pos.dtype == torch.int64
+    if not (pos64 or pos.dtype == torch.int32) or pos.get_device() != dev:
         raise ValueError("positions: int32 or int64 on q's device")
-    sections = [freq.numel()] if rot.sections is None else [int(n) for n in rot.sections]
-    A = len(sections)
-    if A < 1 or A > 4 or sum(sections) != freq.numel():
+    sec = [pairs] if sections is None else [int(n) for n in sections]
+    A = len(sec)
+    if A < 1 or A > 4 or sum(sec) != pairs:
         raise ValueError("sections: one to four counts that add up to inv_freq's length")
-    # one axis may leave out the axis dimension, and a batch shared positions
+    sec += [0] * (4 - A)
+    # extents and strides (axis, b, n); one axis may leave out the axis
+    # dimension, and then also the batch's
+    ps, pst = list(pos.shape), list(pos.stride())
     full = 2 if packed else 3
-    if pos.dim() < full and A == 1:
-        pos = pos[None]
-    if pos.dim() == 2 and not packed:
-        pos = pos[:, None] if pos.shape[0] == A and A == 1 else pos
-    want = (A, N) if packed else (A, B, N)
-    if pos.dim() != full or any(p != w and not (i == 1 and not packed and p == 1)
-                                for i, (p, w) in enumerate(zip(pos.shape, want))):
-        raise ValueError(f"positions: expected {list(want)}, got {list(rot.positions.shape)}")
-    if packed:
-        pos = pos[:, None]
-    pr = RotaryProblem()
-    pr.B, pr.N, pr.Hq, pr.Hkv, pr.D = B, N, Hq, k4.shape[1], D
-    pr.dtype, pr.interleaved = _DTYPE_CODE[q.dtype], int(bool(rot.interleaved))
-    pr.n_axes = A
-    for i, n in enumerate(sections):
-        pr.sections[i] = n
-    pr.inv_freq, pr.positions = freq.data_ptr(), pos.data_ptr()
-    pr.positions_64 = int(pos.dtype == torch.int64)
-    for i in range(3):
-        pr.pos_stride[i] = pos.stride(i) if pos.shape[i] > 1 else 0
-    if (rot.q_weight is None) != (rot.k_weight is None):
-        raise ValueError("q_weight and k_weight: both or none")
-    if rot.q_weight is not None:
-        for w in (rot.q_weight, rot.k_weight):
-            if w.device != q.device or tuple(w.shape) != (D,) or not w.is_contiguous() \
-                    or w.dtype not in (torch.float32, q.dtype) or w.dtype != rot.q_weight.dtype:
+    while A == 1 and len(ps) < full:
+        ps.insert(0, 1)
+        pst.insert(0, 0)
+    if packed and len(ps) == 2:
+        ps.insert(1, 1)
+        pst.insert(1, 0)
+    if len(ps) != 3 or ps[0] != A or ps[2] != N or (ps[1] != B and ps[1] != 1):
+        raise ValueError(f"positions: expected {[A, N] if packed else [A, B, N]}, got {list(pos.shape)}")
+    if ps[1] != B:
+        pst[1] = 0
+    wq = wk = w32 = 0
+    if qw is not None or kw is not None:
+        if qw is None or kw is None:
+            raise ValueError("q_weight and k_weight: both or none")
+        for w in (qw, kw):
+            if w.get_device() != dev or w.dim() != 1 or w.numel() != D or not w.is_contiguous() \
+                    or (w.dtype != torch.float32 and w.dtype != dt) or w.dtype != qw.dtype:
                 raise ValueError("q_weight, k_weight: contiguous [D] of one dtype, float32 or q's")
-        pr.q_weight, pr.k_weight = rot.q_weight.data_ptr(), rot.k_weight.data_ptr()
-        pr.weight_f32 = int(rot.q_weight.dtype == torch.float32)
-    pr.eps = float(rot.eps)
-    return pr, packed
+        wq, wk, w32 = qw.data_ptr(), kw.data_ptr(), qw.dtype == torch.float32
+    return _PACK_ROTARY(B, N, Hq, Hkv, D, _DTYPE_CODE[dt], bool(interleaved), A, *sec,
+                        freq.data_ptr(), pos.data_ptr(), *pst, pos64, w32, wq, wk, float(eps))
 
 
 def _rotary_out(x, out):
@@ -470,42 +515,39 @@ def _rotary_out(x, out):
 
 
 def _apply_fwd(q, k, rot, out):
-    pr, packed = _rotary_problem(q, k, rot)
-    qo, ko = (_rotary_out(x, o) for x, o in zip((q, k), out or (None, None)))
-    t4 = [_as4(t, packed) for t in (q, k, qo, ko)]
-    lib = load_library()
-    with torch.cuda.device(q.device):
-        code = lib.fa_rotary_fwd(ctypes.byref(pr), *(a for t in t4 for a in (t.data_ptr(), _strides(t))),
-                                 _stream(q))
-    _check(code, "fa_rotary_fwd")
+    pr = _rotary_problem(q, k, rot)
+    qo, ko = out or (None, None)
+    qo, ko = _rotary_out(q, qo), _rotary_out(k, ko)
+    _call(load_library().fa_rotary_fwd, "fa_rotary_fwd", q.get_device(), pr, q.data_ptr(),
+          _strides4(q), k.data_ptr(), _strides4(k), qo.data_ptr(), _strides4(qo), ko.data_ptr(),
+          _strides4(ko))
     return qo, ko
 
 
 def _apply_bwd(q, k, dqo, dko, rot, out):
-    """q, k are not read when rot has no weights (and may be the gradients)."""
-    pr, packed = _rotary_problem(dqo, dko, rot)
+    """q, k are not read when rot has no weights (and may be None)."""
+    pr = _rotary_problem(dqo, dko, rot)
     norm = rot.q_weight is not None
     if norm:
         for x, g in ((q, dqo), (k, dko)):
             if x.shape != g.shape or x.dtype != g.dtype or x.device != g.device:
                 raise ValueError("gradients: the shape, dtype and device of their inputs")
-    dq, dk = (_rotary_out(x, o) for x, o in zip((dqo, dko), out or (None, None)))
-    D = dqo.shape[-1]
+    dq, dk = out or (None, None)
+    dq, dk = _rotary_out(dqo, dq), _rotary_out(dko, dk)
     lib = load_library()
-    dw = ws = None
-    nbytes = 0
     if norm:
+        D = dqo.shape[-1]
         dw = torch.empty((2, D), dtype=torch.float32, device=q.device)
-        nbytes = int(lib.fa_rotary_bwd_workspace_bytes(ctypes.byref(pr)))
-        ws = torch.empty(max(nbytes // 4, 4), dtype=torch.float32, device=q.device)
-    t4 = [_as4(t, packed) for t in (q if norm else dqo, k if norm else dko, dqo, dko, dq, dk)]
-    with torch.cuda.device(dqo.device):
-        code = lib.fa_rotary_bwd(ctypes.byref(pr),
-                                 *(a for t in t4 for a in (t.data_ptr(), _strides(t))),
-                                 dw[0].data_ptr() if norm else None,
-                                 dw[1].data_ptr() if norm else None,
-                                 ws.data_ptr() if norm else None, nbytes, _stream(dqo))
-    _check(code, "fa_rotary_bwd")
+        nbytes = lib.fa_rotary_bwd_workspace_bytes(pr)
+        ws = torch.empty(nbytes // 4, dtype=torch.float32, device=q.device)
+        dw0 = dw.data_ptr()
+        extra = (dw0, dw0 + 4 * D, ws.data_ptr(), nbytes)
+    else:
+        q, k = dqo, dko
+        extra = (0, 0, 0, 0)
+    _call(lib.fa_rotary_bwd, "fa_rotary_bwd", dqo.get_device(), pr, q.data_ptr(), _strides4(q),
+          k.data_ptr(), _strides4(k), dqo.data_ptr(), _strides4(dqo), dko.data_ptr(), _strides4(dko),
+          dq.data_ptr(), _strides4(dq), dk.data_ptr(), _strides4(dk), *extra)
     return (dq, dk, dw[0], dw[1]) if norm else (dq, dk)
 
 
@@ -591,33 +633,29 @@ def qk_norm_rotary(q, k, q_weight, k_weight, positions, inv_freq, sections=None,
 # Serving: new tokens over a shared prefix and each request's own rows
 
 
-def _decode_problem(q, k_prefix, k, seq_lens, causal, scale):
-    if q.dtype not in (torch.float16, torch.bfloat16) or not q.is_cuda:
-        raise TypeError("decode takes CUDA float16 or bfloat16 tensors")
-    if q.dim() != 4 or k.dim() != 4 or k_prefix.dim() != 3:
+def _decode_sizes(q, k_prefix, k):
+    """(B, Hq, Hkv, Nq, D, P, S) of a decode call."""
+    qs, ps, ks = q.shape, k_prefix.shape, k.shape
+    if len(qs) != 4 or len(ks) != 4 or len(ps) != 3:
         raise ValueError("expected q [B, Hq, Nq, D], k, v [B, Hkv, S, D], prefixes [Hkv, P, D]")
-    B, Hq, Nq, D = q.shape
-    if k.shape[0] != B or k.shape[3] != D or k_prefix.shape[0] != k.shape[1] \
-            or k_prefix.shape[2] != D:
+    B, Hq, Nq, D = qs
+    Hkv, P, Dp = ps
+    if ks[0] != B or ks[1] != Hkv or ks[3] != D or Dp != D:
         raise ValueError("q, k and the prefix must share batch, key/value heads and head dimension")
-    pr = DecodeProblem()
-    pr.B, pr.Hq, pr.Hkv, pr.Nq, pr.D = B, Hq, k.shape[1], Nq, D
-    pr.P, pr.S = k_prefix.shape[1], k.shape[2]
-    if seq_lens is not None:
-        if seq_lens.dtype != torch.int32 or tuple(seq_lens.shape) != (B,) \
-                or seq_lens.device != q.device or not seq_lens.is_contiguous():
-            raise ValueError("seq_lens: a contiguous int32 vector of B lengths on q's device")
-        pr.seq_lens = seq_lens.data_ptr()
-    pr.causal, pr.scale, pr.dtype = int(bool(causal)), _scale(D, scale), _DTYPE_CODE[q.dtype]
-    return pr
+    return B, Hq, Hkv, Nq, D, P, ks[2]
+
+
+@functools.lru_cache(maxsize=256)
+def _decode_bytes(sizes) -> int:
+    # the lengths, type and scale do not change the size
+    pr = _PACK_DECODE(*sizes, 16, 1, 1.0, FA_F16)
+    return int(load_library().fa_decode_workspace_bytes(pr))
 
 
 def decode_workspace_bytes(q, k_prefix, k) -> int:
     """Bytes of the workspace decode needs for these shapes (0 if invalid, or
     without a prefix)."""
-    pr = _decode_problem(q, k_prefix, k, None, True, None)
-    pr.seq_lens = 16           # its contents do not matter here
-    return int(load_library().fa_decode_workspace_bytes(ctypes.byref(pr)))
+    return _decode_bytes(_decode_sizes(q, k_prefix, k))
 
 
 def decode(q, k_prefix, v_prefix, k, v, seq_lens, o, lse, causal: bool = True, scale=None, *,
@@ -625,31 +663,34 @@ def decode(q, k_prefix, v_prefix, k, v, seq_lens, o, lse, causal: bool = True, s
     """fa_decode.  workspace: a contiguous CUDA tensor of at least
     decode_workspace_bytes(q, k_prefix, k) bytes, 16-byte aligned (None when
     that is 0); calls that may overlap on the GPU need one each."""
-    pr = _decode_problem(q, k_prefix, k, seq_lens, causal, scale)
-    for ref, ts in ((q, (o,)), (k, (v,)), (k_prefix, (v_prefix,))):
-        for t in ts:
-            if t.shape != ref.shape:
-                raise ValueError("o, v and v_prefix take the shapes of q, k and k_prefix")
+    dt = q.dtype
+    if (dt != torch.bfloat16 and dt != torch.float16) or not q.is_cuda:
+        raise TypeError("decode takes CUDA float16 or bfloat16 tensors")
+    sizes = _decode_sizes(q, k_prefix, k)
+    dev = q.get_device()
     for t in (k_prefix, v_prefix, k, v, o):
-        if t.dtype != q.dtype or t.device != q.device:
+        if t.dtype != dt or t.get_device() != dev:
             raise ValueError("all tensors must share dtype and device")
-    if lse.dtype != torch.float32 or lse.shape != q.shape[:3] or lse.device != q.device \
+    if o.shape != q.shape or v.shape != k.shape or v_prefix.shape != k_prefix.shape:
+        raise ValueError("o, v and v_prefix take the shapes of q, k and k_prefix")
+    if lse.dtype != torch.float32 or lse.shape != q.shape[:3] or lse.get_device() != dev \
             or not lse.is_contiguous():
         raise ValueError("lse: contiguous float32 [B, Hq, Nq] on q's device")
-    nbytes = 0
+    if seq_lens.dtype != torch.int32 or seq_lens.dim() != 1 or seq_lens.numel() != sizes[0] \
+            or seq_lens.get_device() != dev or not seq_lens.is_contiguous():
+        raise ValueError("seq_lens: a contiguous int32 vector of B lengths on q's device")
+    ws = nbytes = 0
     if workspace is not None:
-        if workspace.device != q.device or not workspace.is_contiguous():
+        if workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError("workspace: a contiguous tensor on q's device")
-        nbytes = workspace.numel() * workspace.element_size()
-    lib = load_library()
-    args = []
-    for t in (q, k_prefix[None], v_prefix[None], k, v, o):
-        args += [t.data_ptr(), _strides(t)]
-    with torch.cuda.device(q.device):
-        code = lib.fa_decode(ctypes.byref(pr), *args, lse.data_ptr(),
-                             workspace.data_ptr() if workspace is not None else None, nbytes,
-                             _stream(q))
-    _check(code, "fa_decode")
+        ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    pr = _PACK_DECODE(*sizes, seq_lens.data_ptr(), bool(causal), _scale(sizes[4], scale),
+                      _DTYPE_CODE[dt])
+    sp, svp = k_prefix.stride(), v_prefix.stride()
+    _call(load_library().fa_decode, "fa_decode", dev, pr, q.data_ptr(), _PACK4(*q.stride()),
+          k_prefix.data_ptr(), _PACK4(0, *sp), v_prefix.data_ptr(), _PACK4(0, *svp), k.data_ptr(),
+          _PACK4(*k.stride()), v.data_ptr(), _PACK4(*v.stride()), o.data_ptr(),
+          _PACK4(*o.stride()), lse.data_ptr(), ws, nbytes)
 
 
 def attention_decode(q, k_prefix, v_prefix, k, v, seq_lens, causal: bool = True, scale=None,
@@ -660,10 +701,11 @@ def attention_decode(q, k_prefix, v_prefix, k, v, seq_lens, causal: bool = True,
     requests' own cache rows, of which request b's first seq_lens[b] count (int32
     CUDA vector; the new tokens' rows among them, as the last Nq).  causal: token
     t sees own rows up to its own.  float16 and bfloat16; no gradient."""
-    o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    lse = torch.empty(q.shape[:3], dtype=torch.float32, device=q.device)
+    sizes = _decode_sizes(q, k_prefix, k)
+    o = torch.empty_like(q, memory_format=torch.contiguous_format)
+    lse = torch.empty(sizes[0], sizes[1], sizes[3], dtype=torch.float32, device=q.device)
     if workspace is None:
-        nbytes = decode_workspace_bytes(q, k_prefix, k)
+        nbytes = _decode_bytes(sizes)
         if nbytes:
             workspace = torch.empty(nbytes // 4, dtype=torch.float32, device=q.device)
     decode(q, k_prefix, v_prefix, k, v, seq_lens, o, lse, causal, scale, workspace=workspace)
@@ -934,3 +976,136 @@ def attention_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int,
               max_seqlen_q=max_seqlen_q, max_seqlen_k=max_seqlen_k,
               dropout_p=dropout_p, seed=seed, offset=offset)
     return _AttentionEx.apply(q, k, v, causal, scale, kw, deterministic, keep_mask)
+
+
+# ----------------------------------------------------------------------------
+# Packed sequences behind one shared prefix
+
+
+def _prefix_problem(q, k, k_prefix, cu_q, cu_k, max_q, max_k, causal, scale) -> bytes:
+    """struct fa_problem of a prefix call, its tensors' common checks done."""
+    dt = q.dtype
+    if dt not in _DTYPE_CODE or not q.is_cuda:
+        raise TypeError("tensors must be CUDA float32, float16 or bfloat16")
+    if q.dim() != 3 or k.dim() != 3 or k_prefix.dim() != 3:
+        raise ValueError("expected q [total_q, Hq, D], k, v [total_k, Hkv, D], prefixes [P, Hkv, D]")
+    dev = q.get_device()
+    total_q, Hq, D = q.shape
+    total_k, Hkv, Dk = k.shape
+    if Dk != D or k_prefix.shape[1] != Hkv or k_prefix.shape[2] != D:
+        raise ValueError("q, k and the prefix must share head dimension and key/value heads")
+    for cu in (cu_q, cu_k):
+        if cu.dtype != torch.int32 or cu.get_device() != dev or cu.dim() != 1 \
+                or not cu.is_contiguous() or cu.numel() != cu_q.numel() or cu.numel() < 2:
+            raise ValueError("cu_seqlens_q and cu_seqlens_k: contiguous int32 CUDA vectors of B+1")
+    return _PACK_PROBLEM(cu_q.numel() - 1, Hq, Hkv, int(max_q), int(max_k), D, cu_q.data_ptr(),
+                         cu_k.data_ptr(), total_q, total_k, bool(causal), _scale(D, scale),
+                         _DTYPE_CODE[dt], 0.0, 0, 0, 0)
+
+
+def _like(ref, *ts):
+    for t in ts:
+        if t.shape != ref.shape or t.dtype != ref.dtype or t.device != ref.device:
+            raise ValueError("tensors of one kind must share shape, dtype and device")
+
+
+def _lse_like(q, *ts):
+    for t in ts:
+        if t.dtype != torch.float32 or t.device != q.device or not t.is_contiguous() \
+                or tuple(t.shape) != (q.shape[1], q.shape[0]):
+            raise ValueError("lse, delta: contiguous float32 [Hq, total_q] on q's device")
+
+
+def _addr(*ts):
+    """Address and strides of packed tensors, in turn."""
+    return [x for t in ts for x in (t.data_ptr(), _strides4(t))]
+
+
+def fwd_prefix(q, k, v, k_prefix, v_prefix, o, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
+               max_seqlen_k, causal: bool = True, scale=None):
+    """fa_fwd_prefix: q, o [total_q, Hq, D], k, v [total_k, Hkv, D], k_prefix,
+    v_prefix [P, Hkv, D], lse [Hq, total_q]."""
+    pr = _prefix_problem(q, k, k_prefix, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k,
+                         causal, scale)
+    _like(q, o)
+    _like(k, v)
+    _like(k_prefix, v_prefix)
+    _lse_like(q, lse)
+    if k.dtype != q.dtype or k_prefix.dtype != q.dtype or k.device != q.device \
+            or k_prefix.device != q.device:
+        raise ValueError("all tensors must share dtype and device")
+    _call(load_library().fa_fwd_prefix, "fa_fwd_prefix", q.get_device(), pr, k_prefix.shape[0],
+          *_addr(q, k_prefix, v_prefix, k, v, o), lse.data_ptr())
+
+
+def bwd_prefix(q, k, v, k_prefix, v_prefix, do, lse, delta, dq, dk, dv, dk_prefix, dv_prefix,
+               cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, causal: bool = True,
+               scale=None):
+    """fa_bwd_prefix: the gradients of fwd_prefix from its lse and delta =
+    rowsum(do * o), [Hq, total_q]."""
+    pr = _prefix_problem(q, k, k_prefix, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k,
+                         causal, scale)
+    _like(q, do, dq)
+    _like(k, v, dk, dv)
+    _like(k_prefix, v_prefix, dk_prefix, dv_prefix)
+    _lse_like(q, lse, delta)
+    if k.dtype != q.dtype or k_prefix.dtype != q.dtype or k.device != q.device \
+            or k_prefix.device != q.device:
+        raise ValueError("all tensors must share dtype and device")
+    _call(load_library().fa_bwd_prefix, "fa_bwd_prefix", q.get_device(), pr, k_prefix.shape[0],
+          *_addr(q, k_prefix, v_prefix, k, v, do), lse.data_ptr(), delta.data_ptr(),
+          *_addr(dq, dk_prefix, dv_prefix, dk, dv))
+
+
+def attention_prefix_fwd(q, k, v, k_prefix, v_prefix, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
+                         max_seqlen_k, causal: bool = True, scale=None):
+    """Allocating fwd_prefix: (o, lse)."""
+    o = torch.empty_like(q, memory_format=torch.contiguous_format)
+    lse = torch.empty(q.shape[1], q.shape[0], dtype=torch.float32, device=q.device)
+    fwd_prefix(q, k, v, k_prefix, v_prefix, o, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
+               max_seqlen_k, causal, scale)
+    return o, lse
+
+
+def attention_prefix_bwd(q, k, v, k_prefix, v_prefix, o, lse, do, cu_seqlens_q, cu_seqlens_k,
+                         max_seqlen_q, max_seqlen_k, causal: bool = True, scale=None):
+    """Allocating bwd_prefix: (dq, dk, dv, dk_prefix, dv_prefix)."""
+    delta = torch.empty_like(lse)
+    bwd_preprocess(_as4(o, True), _as4(do, True), delta)
+    dq, dk, dv, dkp, dvp = (torch.empty_like(t, memory_format=torch.contiguous_format)
+                            for t in (q, k, v, k_prefix, v_prefix))
+    bwd_prefix(q, k, v, k_prefix, v_prefix, do, lse, delta, dq, dk, dv, dkp, dvp, cu_seqlens_q,
+               cu_seqlens_k, max_seqlen_q, max_seqlen_k, causal, scale)
+    return dq, dk, dv, dkp, dvp
+
+
+class _AttentionPrefix(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, k, v, k_prefix, v_prefix, cu_q, cu_k, max_q, max_k, causal, scale):
+        o, lse = attention_prefix_fwd(q, k, v, k_prefix, v_prefix, cu_q, cu_k, max_q, max_k, causal,
+                                      scale)
+        ctx.save_for_backward(q, k, v, k_prefix, v_prefix, o, lse, cu_q, cu_k)
+        ctx.args = (max_q, max_k, causal, scale)
+        return o
+
+    @staticmethod
+    @torch.autograd.function.once_differentiable
+    def backward(ctx, do):
+        q, k, v, kp, vp, o, lse, cu_q, cu_k = ctx.saved_tensors
+        grads = attention_prefix_bwd(q, k, v, kp, vp, o, lse, _dense(do), cu_q, cu_k, *ctx.args)
+        return (*grads, None, None, None, None, None, None)
+
+
+def attention_varlen_prefix(q, k, v, k_prefix, v_prefix, cu_seqlens_q, cu_seqlens_k,
+                            max_seqlen_q: int, max_seqlen_k: int, causal: bool = True, scale=None,
+                            rotary: Optional[Rotary] = None):
+    """Autograd attention over packed sequences that share a prefix: q
+    [total_q, Hq, D], k, v [total_k, Hkv, D], k_prefix, v_prefix [P, Hkv, D]
+    (every query sees all of it; its gradients sum over the sequences),
+    cu_seqlens_* int32 CUDA offsets (B+1).  causal: within each sequence, counted
+    from its first row.  rotary: the rotation (and head norm) to apply to q and k
+    first (not to the prefix, which is used as it is)."""
+    if rotary is not None:
+        q, k = apply_rotary(q, k, rotary)
+    return _AttentionPrefix.apply(*(_dense(t) for t in (q, k, v, k_prefix, v_prefix)), cu_seqlens_q,
+                                  cu_seqlens_k, max_seqlen_q, max_seqlen_k, causal, scale)

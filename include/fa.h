@@ -334,6 +334,43 @@ FA_API fa_status fa_dropout_mask(const fa_problem* prob, uint8_t* mask, size_t b
                                  cudaStream_t stream);
 
 /*
+ * Packed sequences behind one shared prefix (the answers to one long prompt, a
+ * batch of questions about one document): every query sees all P prefix keys
+ * and, within its own sequence, the keys that `prob` describes; one softmax
+ * over both.  `prob` must be packed (cu_seqlens_* set) and without dropout.
+ *
+ *   q, o, dout, dq                    [1, Hq, total_q, D] views as for fa_fwd_ex
+ *   k, v, dk, dv                      [1, Hkv, total_k, D] views
+ *   k_prefix, v_prefix, dk_prefix, dv_prefix   [1, Hkv, P, D] views, P >= 0
+ *                                     (P = 0: ignored)
+ *   lse, delta                        fp32 [Hq, total_q]; lse is over both sets of
+ *                                     keys, delta = rowsum(dO o O) as for fa_bwd_ex
+ * Strides and alignment as for fa_fwd, but no stride of 0 over an extent above
+ * 1.  dk_prefix and dv_prefix sum over every sequence.  Results do not depend on
+ * the schedule (no atomics).  Rows that belong to no sequence (before
+ * cu_seqlens[0], past cu_seqlens[B]) are neither used nor written, whatever they
+ * hold.  A sequence whose offsets break
+ * fa_problem's rules is skipped and reported as there (FA_ERR_SEQLENS); the
+ * gradients of the prefix are then not defined.
+ *
+ * Errors as for fa_fwd_ex / fa_bwd_ex, plus FA_ERR_SHAPE for P < 0 or sequences
+ * that are not packed, FA_ERR_ARG for dropout_p > 0.
+ */
+FA_API fa_status fa_fwd_prefix(const fa_problem* prob, int64_t P, const void* q, const int64_t* sq,
+                               const void* k_prefix, const int64_t* skp, const void* v_prefix,
+                               const int64_t* svp, const void* k, const int64_t* sk, const void* v,
+                               const int64_t* sv, void* o, const int64_t* so, float* lse,
+                               cudaStream_t stream);
+FA_API fa_status fa_bwd_prefix(const fa_problem* prob, int64_t P, const void* q, const int64_t* sq,
+                               const void* k_prefix, const int64_t* skp, const void* v_prefix,
+                               const int64_t* svp, const void* k, const int64_t* sk, const void* v,
+                               const int64_t* sv, const void* dout, const int64_t* sdo,
+                               const float* lse, const float* delta, void* dq, const int64_t* sdq,
+                               void* dk_prefix, const int64_t* sdkp, void* dv_prefix,
+                               const int64_t* sdvp, void* dk, const int64_t* sdk, void* dv,
+                               const int64_t* sdv, cudaStream_t stream);
+
+/*
  * Rotation of query and key heads by their positions, with one or several
  * axes, and optionally the RMS norm of every head in the same pass.
  *

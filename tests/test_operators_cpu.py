@@ -132,3 +132,62 @@ def test_python_refusals():
         fa.rotary_fwd(x, x, torch.arange(8), torch.ones(32))
     with pytest.raises(TypeError):
         fa.attention_decode(x, x[0], x[0], x, x, torch.zeros(2, dtype=torch.int32))
+
+
+def test_packed_structs_have_the_c_layout():
+    """The binding's packed bytes are the ctypes mirrors of the C structs, field
+    by field."""
+    pr = _rot(n_axes=3, sections=(8, 12, 12, 0), interleaved=1, pos_stride=(7, 5, 3), weight_f32=1,
+              q_weight=FAKE + 16, k_weight=FAKE + 32, eps=0.25)
+    raw = fa._PACK_ROTARY(2, 10, 4, 2, 64, 2, 1, 3, 8, 12, 12, 0, FAKE, FAKE, 7, 5, 3, 1, 1, FAKE + 16,
+                          FAKE + 32, 0.25)
+    assert raw == bytes(pr)
+    raw = fa._PACK_DECODE(2, 4, 2, 1, 64, 100, 10, FAKE, 1, 0.125, 2)
+    assert raw[:76] == bytes(_dec())[:76] and len(raw) == len(bytes(_dec()))
+    pr = _packed()
+    pr.seed, pr.offset = 5, 6
+    raw = fa._PACK_PROBLEM(3, 4, 2, 40, 50, 64, FAKE, FAKE, 100, 120, 1, 0.125, 2, 0.0, 5, 6, 0)
+    assert raw == bytes(pr)
+
+
+def _packed(**kw):
+    pr = fa.Problem()
+    d = dict(B=3, Hq=4, Hkv=2, Nq=40, Nk=50, D=64, cu_seqlens_q=FAKE, cu_seqlens_k=FAKE, total_q=100,
+             total_k=120, causal=1, scale=0.125, dtype=2)
+    d.update(kw)
+    for name, v in d.items():
+        setattr(pr, name, v)
+    return pr
+
+
+def test_prefix_validation(lib):
+    st = S4(0, 64, 256, 1)
+
+    def fwd(pr, P=70, q=FAKE, kp=FAKE, skp=st, so=st, lse=FAKE):
+        return lib.fa_fwd_prefix(ctypes.byref(pr) if pr is not None else None, P, q, st, kp, skp, FAKE, st,
+                                 FAKE, st, FAKE, st, FAKE, so, lse, None)
+
+    def bwd(pr, P=70, dkp=FAKE, sdk=st, delta=FAKE, dq=FAKE):
+        return lib.fa_bwd_prefix(ctypes.byref(pr), P, FAKE, st, FAKE, st, FAKE, st, FAKE, st, FAKE, st, FAKE,
+                                 st, FAKE, delta, dq, st, dkp, st, FAKE, st, FAKE, sdk, FAKE, st, None)
+
+    assert fwd(None) == 1
+    for call in (fwd, bwd):
+        for kw, code in ((dict(dtype=9), 4), (dict(Hkv=3), 2), (dict(D=48), 3), (dict(scale=0.0), 10),
+                         (dict(cu_seqlens_k=None), 2), (dict(cu_seqlens_q=None, cu_seqlens_k=None), 2),
+                         (dict(dropout_p=0.1), 11), (dict(total_q=0), 2)):
+            assert call(_packed(**kw)) == code, kw
+        assert call(_packed(), P=-1) == 2
+        assert call(_packed(), P=1 << 31) == 2
+        assert call(_packed(Nk=1 << 30), P=(1 << 30) + 5) == 2
+    assert fwd(_packed(), q=None) == 1
+    assert fwd(_packed(), kp=None) == 1
+    assert fwd(_packed(), kp=FAKE + 8) == 6
+    assert fwd(_packed(), skp=S4(0, 0, 256, 1)) == 5
+    assert fwd(_packed(), so=S4(0, 64, 0, 1)) == 5
+    assert fwd(_packed(), lse=None) == 1
+    assert fwd(_packed(), P=0, kp=None, lse=None) == 1           # without a prefix its pointers are ignored
+    assert bwd(_packed(), dkp=None) == 1
+    assert bwd(_packed(), sdk=S4(0, 64, 250, 1)) == 6
+    assert bwd(_packed(), delta=None) == 1
+    assert bwd(_packed(), P=0, dkp=None, dq=None) == 1
