@@ -20,7 +20,7 @@
 //    That is bound by HBM at any rate the matrix units run, so its warps load
 //    K and V straight into the registers of m16n8k16 products, 16 bytes per
 //    lane and whole 64- or 128-byte pieces per row, without shared memory, and
-//    many warps per SM keep the loads in flight.  A cluster of up to eight
+//    sixteen warps per SM keep the loads in flight.  A cluster of up to eight
 //    blocks shares one request's rows when there are few requests.  The same
 //    kernel then joins all partial sums and writes o and L.
 //
@@ -56,8 +56,8 @@ struct PreCfg {
   static constexpr int OFF_RING = 2 * TILE;
   // partial sums are staged over the ring: 2 x 128 rows x D fp32
   static constexpr int RING = NS * TILE > 2 * 128 * D * 4 ? NS * TILE : 2 * 128 * D * 4;
-  static constexpr int OFF_ML = OFF_RING + RING;    // (m, l) of group 1's rows
-  static constexpr int OFF_BAR = OFF_ML + 1024;
+  static constexpr int OFF_ML = OFF_RING + RING;    // (m, l) of group 1's rows (at first: row offsets)
+  static constexpr int OFF_BAR = OFF_ML + 2048;
   static constexpr int SMEM = OFF_BAR + 512 + 1024;
   static constexpr uint32_t COL_S0 = 0, COL_O0 = 256;
 };
@@ -100,6 +100,8 @@ __global__ void __launch_bounds__(320, 1)
   const uint32_t b_mmadone = smem_u32(&bars[7 + 2 * C::NS]);
   static_assert(8 + 2 * C::NS <= 32, "barriers below the control block");
 
+  // the own rows' kernel may start as blocks of this one leave
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // blocks of one (head, key range) are neighbours: they read the same tiles
   const int rp = static_cast<int>(blockIdx.x % a.groups);
@@ -270,23 +272,37 @@ __global__ void __launch_bounds__(320, 1)
     // ------------------------------------------------------------ softmax + epilogue
     // Query rows gathered into the operand layout of a 128-byte-swizzled load;
     // columns past a narrow head dimension are zero, rows past R hold whatever
-    // was there (their results are not used).
+    // was there (their results are not used).  Each thread finds one row's
+    // place, then loads eight pieces at a time: with a division and a load per
+    // piece in turn the gather alone took 10 us of a block.
     {
-      const int tile = two ? warp >> 2 : 0;
-      const int nr = nrows[tile];
-      constexpr int UN = D / 8;                       // 16-byte units per row
-      const int tid = two ? threadIdx.x & 127 : threadIdx.x, nth = two ? 128 : 256;
-      for (int idx = tid; idx < nr * UN; idx += nth) {
-        const int r = idx / UN, un = idx % UN;
-        const int row = row0 + 128 * tile + r;
+      int64_t* sRow = reinterpret_cast<int64_t*>(smem + C::OFF_ML);   // (m, l) come later
+      const int nr = nrows[0] + (two ? nrows[1] : 0);
+      if (static_cast<int>(threadIdx.x) < nr) {
+        const int row = row0 + static_cast<int>(threadIdx.x);
         const int b = row / a.GN, rem = row - b * a.GN, hg = rem / a.Nq, tok = rem - hg * a.Nq;
-        uint4 x = make_uint4(0u, 0u, 0u, 0u);
-        if (8 * un < a.dreal)
-          x = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + b * a.sq[0] +
-                                                   static_cast<int64_t>(hk * a.G + hg) * a.sq[1] +
-                                                   tok * a.sq[2] + 8 * un));
-        *reinterpret_cast<uint4*>(sQ + tile * C::TILE + (un >> 3) * C::CHUNK + r * 128 +
-                                  (((un & 7) ^ (r & 7)) << 4)) = x;
+        sRow[threadIdx.x] = b * a.sq[0] + static_cast<int64_t>(hk * a.G + hg) * a.sq[1] + tok * a.sq[2];
+      }
+      bar_red_and(1, 256, true);
+      constexpr int UN = D / 8, RPP = 256 / UN;       // 16-byte units per row, rows per pass
+      const int un = threadIdx.x % UN, rt = threadIdx.x / UN;
+      const bool col = 8 * un < a.dreal;
+      for (int r0 = rt; r0 < nr; r0 += 8 * RPP) {
+        uint4 x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int r = r0 + i * RPP;
+          x[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (r < nr && col)
+            x[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + sRow[r] + 8 * un));
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int rr = r0 + i * RPP, r = rr & 127;
+          if (rr < nr)
+            *reinterpret_cast<uint4*>(sQ + (rr >> 7) * C::TILE + (un >> 3) * C::CHUNK + r * 128 +
+                                      (((un & 7) ^ (r & 7)) << 4)) = x[i];
+        }
       }
       fence_async_smem();
       mbar_arrive(b_q);
@@ -463,18 +479,25 @@ __global__ void __launch_bounds__(320, 1)
 // ============================================================================
 // Own rows, and the join
 // ============================================================================
-// A block of four warps takes 16 query rows of one (request, key/value head);
-// warp w of block `rank` of the cluster takes every (4 * cluster)-th block of
-// 16 keys.  Operand layout of the m16n8k16 products: lane 4 n + c holds, of
-// the K operand, key n's elements in slots 2c, 2c+1, 2c+8, 2c+9 of 16.  The
-// order of the contraction is free, so the slots of two products take the
-// eight elements 8c .. 8c+7 of a 32-element piece: one 16-byte load.  Of the V
-// operand the lane holds keys 2c, 2c+1, 2c+8, 2c+9 for output column n: output
-// column j of product tile n is element 8 n + j, so eight tiles take one
-// 16-byte load of each of the four keys.
+// A block of four warps takes 8 NT query rows of one (request, key/value
+// head); warp w of block `rank` of the cluster takes every (4 * cluster)-th
+// block of 16 keys.  Scores are formed transposed, S^T = K Q^T, and so is the
+// output, O^T = V^T P^T: the keys (then the columns of V) fill the 16 rows of
+// the m16n8k16 products and the few query rows their 8 columns, so that no
+// half of a product is padding for up to eight query rows and the sums take
+// D / 4 registers per lane and tile.
+// Lane 4 g + c holds, of an operand with rows g and g + 8, the elements in
+// slots 2c, 2c+1, 2c+8, 2c+9 of 16.  The order of a contraction is free, so the
+// slots of two products over K take the eight elements 8c .. 8c+7 of a
+// 32-element piece: one 16-byte load.  Of V the lane holds keys 2c, 2c+1, 2c+8,
+// 2c+9; product tile j takes as its rows g and g + 8 the elements 8g + 2j and
+// 8g + 2j + 1 of a 64-element piece, so four tiles share one 16-byte load of
+// each of the four keys.  P^T comes out of S^T with its halves the other way
+// round; movmatrix turns them.
 constexpr int kOwnThreads = 128;
 constexpr int kOwnWarps = kOwnThreads / 32;
 constexpr int kMaxCluster = 8;
+constexpr int kMaxRanges = 64;            // ranges of the prefix
 
 struct OwnArgs {
   const void* q; const void* k; const void* v;
@@ -483,7 +506,7 @@ struct OwnArgs {
   int64_t sq[3], sk[3], sv[3], so[3];
   const int32_t* lens;
   int64_t S;
-  int B, Hq, Hkv, G, Nq, GN, RT;     // RT: 16-row tiles of GN rows
+  int B, Hq, Hkv, G, Nq, GN, RT;     // RT: tiles of 8 NT of the GN rows
   int dreal, causal;
   float c;
   int cluster;
@@ -494,190 +517,223 @@ struct OwnArgs {
 };
 
 template <typename T>
-__device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                         uint32_t b1) {
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
   if constexpr (std::is_same<T, __nv_bfloat16>::value)
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
                  "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
   else
     asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
                  "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// Transposes an 8 x 8 matrix of 16-bit elements, two neighbours of row lane / 4
+// per lane.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 
 __device__ __forceinline__ uint4 ld_stream(const void* p) {
   return __ldcs(static_cast<const uint4*>(p));
 }
+__device__ __forceinline__ uint32_t word(const uint4& v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+// Sum or maximum over the eight lanes of one c.
+__device__ __forceinline__ float max_g(float v) {
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+  v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+  return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+}
+__device__ __forceinline__ float sum_g(float v) {
+  v += __shfl_xor_sync(0xffffffffu, v, 4);
+  v += __shfl_xor_sync(0xffffffffu, v, 8);
+  return v + __shfl_xor_sync(0xffffffffu, v, 16);
+}
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kOwnThreads)
+// Blocks per SM that the registers are kept to.
+constexpr int own_blocks(int D, int NT) {
+  return D == 64 ? (NT == 1 ? 4 : 3) : (NT == 1 ? 3 : 2);
+}
+
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kOwnThreads, own_blocks(D, NT))
     own_kernel(const __grid_constant__ OwnArgs a) {
   constexpr int KP = D / 32;              // 32-element pieces of a K row
   constexpr int VP = D / 64;              // 64-element pieces of a V row
-  constexpr int DO = D;
-  __shared__ __align__(16) float sO[kOwnWarps][16][DO];
-  __shared__ float sL[kOwnWarps][16];     // log2 of each warp's sum, -inf: no key
-  __shared__ float sW[16][kOwnWarps * kMaxCluster];
-  __shared__ float sTot[16];
+  constexpr int ROWS = 8 * NT;
+  __shared__ __align__(16) float sO[kOwnWarps][ROWS][D];
+  __shared__ float sL[kOwnWarps][ROWS];   // log2 of each warp's sum, -inf: no key
+  __shared__ float sW[ROWS][kOwnWarps * kMaxCluster];
+  __shared__ float sP[ROWS][kMaxRanges];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n8 = lane >> 2, c4 = lane & 3;
+  const int g8 = lane >> 2, c4 = lane & 3;
   const int rank = static_cast<int>(blockIdx.x % a.cluster);
   int id = static_cast<int>(blockIdx.x / a.cluster);
   const int rt = id % a.RT;
   id /= a.RT;
   const int hk = id % a.Hkv, b = id / a.Hkv;
-  const int64_t len = a.lens ? __ldg(a.lens + b) : 0;
+  const int len = a.lens ? __ldg(a.lens + b) : 0;
   if (len < 0 || len > a.S) {             // every block of the cluster takes this
     if (threadIdx.x == 0) record_status(a.status, FA_ERR_SEQLENS);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
   }
-  const int r0 = rt * 16;
-  const int nr = a.GN - r0 < 16 ? a.GN - r0 : 16;      // valid rows
+  const int r0 = rt * ROWS;
+  const int nr = a.GN - r0 < ROWS ? a.GN - r0 : ROWS;      // valid rows
 
-  // Q fragments: rows n8 and n8 + 8; piece p, product pair (2p, 2p + 1)
-  uint32_t qa[KP][8];
-  int64_t lim[2];                          // last own key each row sees
-#pragma unroll
-  for (int hf = 0; hf < 2; ++hf) {
-    const int row = n8 + 8 * hf;
-    const bool on = row < nr;
-    const int gr = r0 + (on ? row : 0), hg = gr / a.Nq, tok = gr - hg * a.Nq;
-    lim[hf] = a.causal ? len - a.Nq + tok : len - 1;
-    const T* q = static_cast<const T*>(a.q) + b * a.sq[0] + static_cast<int64_t>(hk * a.G + hg) * a.sq[1] +
-                 tok * a.sq[2];
-#pragma unroll
-    for (int p = 0; p < KP; ++p) {
-      uint4 x = make_uint4(0u, 0u, 0u, 0u);
-      if (on && 32 * p + 8 * c4 < a.dreal) x = __ldg(reinterpret_cast<const uint4*>(q + 32 * p + 8 * c4));
-      qa[p][0 + hf] = x.x; qa[p][2 + hf] = x.y;       // product 2p: slots 2c, 2c+1 and 2c+8, 2c+9
-      qa[p][4 + hf] = x.z; qa[p][6 + hf] = x.w;       // product 2p + 1
-    }
-  }
-  const T* kbase = static_cast<const T*>(a.k) + b * a.sk[0] + hk * a.sk[1];
-  const T* vbase = static_cast<const T*>(a.v) + b * a.sv[0] + hk * a.sv[1];
-  float o[8 * VP][4];                      // tile j of piece p: o[8 p + j]
-#pragma unroll
-  for (int i = 0; i < 8 * VP; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
-
-  const int stride = kOwnWarps * a.cluster;
+  const T* kbase = static_cast<const T*>(a.k) + b * a.sk[0] + hk * a.sk[1] + 8 * c4;
+  const T* vbase = static_cast<const T*>(a.v) + b * a.sv[0] + hk * a.sv[1] + 8 * g8;
+  const int stride = 16 * kOwnWarps * a.cluster;
   uint4 kr[2][KP], vr[4][VP];
-  auto load_k = [&](int64_t key0) {
+  auto load_k = [&](int key0) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const int64_t key = key0 + 8 * t + n8;
+      const int key = key0 + 8 * t + g8;
+      const T* row = kbase + key * a.sk[2];
 #pragma unroll
       for (int p = 0; p < KP; ++p)
-        kr[t][p] = key < len && 32 * p + 8 * c4 < a.dreal
-                       ? ld_stream(kbase + key * a.sk[2] + 32 * p + 8 * c4)
-                       : make_uint4(0u, 0u, 0u, 0u);
+        kr[t][p] = key < len && 32 * p + 8 * c4 < a.dreal ? ld_stream(row + 32 * p)
+                                                          : make_uint4(0u, 0u, 0u, 0u);
     }
   };
-  auto load_v = [&](int64_t key0) {
+  auto load_v = [&](int key0) {
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      const int64_t key = key0 + 2 * c4 + (t & 1) + 8 * (t >> 1);
+      const int key = key0 + 2 * c4 + (t & 1) + 8 * (t >> 1);
+      const T* row = vbase + key * a.sv[2];
 #pragma unroll
       for (int p = 0; p < VP; ++p)
-        vr[t][p] = key < len && 64 * p + 8 * n8 < a.dreal
-                       ? ld_stream(vbase + key * a.sv[2] + 64 * p + 8 * n8)
-                       : make_uint4(0u, 0u, 0u, 0u);
+        vr[t][p] = key < len && 64 * p + 8 * g8 < a.dreal ? ld_stream(row + 64 * p)
+                                                          : make_uint4(0u, 0u, 0u, 0u);
     }
   };
-  const int64_t first = static_cast<int64_t>(rank * kOwnWarps + warp) * 16;
+  const int first = (rank * kOwnWarps + warp) * 16;
   if (first < len) load_k(first);
-  for (int64_t key0 = first; key0 < len; key0 += 16 * stride) {
-    load_v(key0);
-    float s[2][4];
+  // Query rows as the second operand: row 8 nt + g, the same pieces as K's
+  uint4 qr[NT][KP];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+  for (int nt = 0; nt < NT; ++nt) {
+    const int row = 8 * nt + g8;
+    const bool on = row < nr;
+    const int gr = r0 + (on ? row : 0), hg = gr / a.Nq, tok = gr - hg * a.Nq;
+    const T* q = static_cast<const T*>(a.q) + b * a.sq[0] + static_cast<int64_t>(hk * a.G + hg) * a.sq[1] +
+                 tok * a.sq[2] + 8 * c4;
+#pragma unroll
+    for (int p = 0; p < KP; ++p)
+      qr[nt][p] = on && 32 * p + 8 * c4 < a.dreal ? __ldg(reinterpret_cast<const uint4*>(q + 32 * p))
+                                                  : make_uint4(0u, 0u, 0u, 0u);
+  }
+  int lim[NT][2];                          // last own key that query rows 8 nt + 2 c4 + e see
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      lim[nt][e] = a.causal ? len - a.Nq + (r0 + 8 * nt + 2 * c4 + e) % a.Nq : len - 1;
+  float o[4 * VP][NT][4];
+#pragma unroll
+  for (int i = 0; i < 4 * VP; ++i)
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) o[i][nt][0] = o[i][nt][1] = o[i][nt][2] = o[i][nt][3] = 0.f;
+  float m[NT][2], l[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    m[nt][0] = m[nt][1] = -INFINITY;
+    l[nt][0] = l[nt][1] = 0.f;
+  }
+
+  for (int key0 = first; key0 < len; key0 += stride) {
+    load_v(key0);
+    float s[NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
 #pragma unroll
       for (int p = 0; p < KP; ++p) {
-        const uint32_t a0[4] = {qa[p][0], qa[p][1], qa[p][2], qa[p][3]};
-        const uint32_t a1[4] = {qa[p][4], qa[p][5], qa[p][6], qa[p][7]};
-        mma16816<T>(s[t], a0, kr[t][p].x, kr[t][p].y);
-        mma16816<T>(s[t], a1, kr[t][p].z, kr[t][p].w);
+        mma16816<T>(s[nt], kr[0][p].x, kr[1][p].x, kr[0][p].y, kr[1][p].y, qr[nt][p].x, qr[nt][p].y);
+        mma16816<T>(s[nt], kr[0][p].z, kr[1][p].z, kr[0][p].w, kr[1][p].w, qr[nt][p].z, qr[nt][p].w);
       }
     }
-    if (key0 + 16 * stride < len) load_k(key0 + 16 * stride);
-    // rows n8 (elements 0, 1) and n8 + 8 (elements 2, 3); keys 8 t + 2 c4 + {0, 1}
-    uint32_t pa[4];
+    if (key0 < len - stride) load_k(key0 + stride);
+    uint32_t pb[NT][2];
+    float alpha[NT][2];
+    bool moved = false;
 #pragma unroll
-    for (int hf = 0; hf < 2; ++hf) {
-      float x[4];
+    for (int nt = 0; nt < NT; ++nt) {
+      float p[2][2];                       // key g8 + 8 t, query row 2 c4 + e
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+      for (int e = 0; e < 2; ++e) {
+        float x[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int64_t key = key0 + 8 * t + 2 * c4 + e;
-          x[2 * t + e] = key <= lim[hf] ? s[t][2 * hf + e] * a.c : -INFINITY;
-        }
-      float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      const float mn = fmaxf(m[hf], mx);
-      // no key seen yet: exponents against 0, so that -inf stays a weight of 0
-      const float ms = mn == -INFINITY ? 0.f : mn;
-      const float alpha = ex2(m[hf] - ms);
-      m[hf] = mn;
-      float sum = 0.f;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        x[i] = ex2(x[i] - ms);
-        sum += x[i];
+        for (int t = 0; t < 2; ++t)
+          x[t] = key0 + 8 * t + g8 <= lim[nt][e] ? s[nt][2 * t + e] * a.c : -INFINITY;
+        const float mn = fmaxf(m[nt][e], max_g(fmaxf(x[0], x[1])));
+        // no key seen yet: exponents against 0, so that -inf stays a weight of 0
+        const float ms = mn == -INFINITY ? 0.f : mn;
+        alpha[nt][e] = ex2(m[nt][e] - ms);
+        moved |= mn != m[nt][e];
+        m[nt][e] = mn;
+        p[0][e] = ex2(x[0] - ms);
+        p[1][e] = ex2(x[1] - ms);
+        l[nt][e] = fmaf(l[nt][e], alpha[nt][e], p[0][e] + p[1][e]);
       }
-      l[hf] = fmaf(l[hf], alpha, sum);
       // P rounded to the input type for the product, as the forward does
-      pa[hf] = pack2<T>(x[0], x[1]);
-      pa[2 + hf] = pack2<T>(x[2], x[3]);
-#pragma unroll
-      for (int i = 0; i < 8 * VP; ++i) {
-        o[i][2 * hf] *= alpha;
-        o[i][2 * hf + 1] *= alpha;
-      }
+      pb[nt][0] = transpose8x8(pack2<T>(p[0][0], p[0][1]));
+      pb[nt][1] = transpose8x8(pack2<T>(p[1][0], p[1][1]));
     }
+    if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-    for (int p = 0; p < VP; ++p) {
+      for (int i = 0; i < 4 * VP; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t sel = (j & 1) ? 0x7632u : 0x5410u;
-        const uint32_t* v0 = &vr[0][p].x;
-        const uint32_t* v1 = &vr[1][p].x;
-        const uint32_t* v2 = &vr[2][p].x;
-        const uint32_t* v3 = &vr[3][p].x;
-        mma16816<T>(o[8 * p + j], pa, prmt(v0[j >> 1], v1[j >> 1], sel),
-                    prmt(v2[j >> 1], v3[j >> 1], sel));
-      }
+        for (int nt = 0; nt < NT; ++nt) {
+          o[i][nt][0] *= alpha[nt][0];
+          o[i][nt][1] *= alpha[nt][1];
+          o[i][nt][2] *= alpha[nt][0];
+          o[i][nt][3] *= alpha[nt][1];
+        }
     }
-  }
-  // This warp's sums, normalised, with log2 of the sum of exponentials
-#pragma unroll
-  for (int hf = 0; hf < 2; ++hf) {
-    l[hf] += __shfl_xor_sync(0xffffffffu, l[hf], 1);
-    l[hf] += __shfl_xor_sync(0xffffffffu, l[hf], 2);
-    const int row = n8 + 8 * hf;
-    const bool none = m[hf] == -INFINITY && l[hf] == 0.f;      // no key seen
-    const float inv = none ? 0.f : 1.f / l[hf];
-    if (c4 == 0) sL[warp][row] = none ? -INFINITY : m[hf] + log2f(l[hf]);
-    // element e of tile j: column n = 2 c4 + e, that is element 8 n + j
 #pragma unroll
     for (int p = 0; p < VP; ++p)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float* dst = &sO[warp][row][64 * p + 8 * (2 * c4 + e)];
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t v0 = word(vr[0][p], j), v1 = word(vr[1][p], j), v2 = word(vr[2][p], j),
+                       v3 = word(vr[3][p], j);
+        const uint32_t a0 = prmt(v0, v1, 0x5410u), a1 = prmt(v0, v1, 0x7632u),
+                       a2 = prmt(v2, v3, 0x5410u), a3 = prmt(v2, v3, 0x7632u);
 #pragma unroll
-        for (int j = 0; j < 8; j += 4)
-          *reinterpret_cast<float4*>(dst + j) =
-              make_float4(o[8 * p + j][2 * hf + e] * inv, o[8 * p + j + 1][2 * hf + e] * inv,
-                          o[8 * p + j + 2][2 * hf + e] * inv, o[8 * p + j + 3][2 * hf + e] * inv);
+        for (int nt = 0; nt < NT; ++nt)
+          mma16816<T>(o[4 * p + j][nt], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
       }
   }
+  // This warp's sums, normalised, with log2 of the sum of exponentials
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float ls = sum_g(l[nt][e]);
+      const int row = 8 * nt + 2 * c4 + e;
+      const bool none = m[nt][e] == -INFINITY && ls == 0.f;      // no key seen
+      const float inv = none ? 0.f : 1.f / ls;
+      if (g8 == 0) sL[warp][row] = none ? -INFINITY : m[nt][e] + log2f(ls);
+#pragma unroll
+      for (int p = 0; p < VP; ++p) {
+        float4* dst = reinterpret_cast<float4*>(&sO[warp][row][64 * p + 8 * g8]);
+#pragma unroll
+        for (int j = 0; j < 4; j += 2)
+          dst[j / 2] = make_float4(o[4 * p + j][nt][e] * inv, o[4 * p + j][nt][2 + e] * inv,
+                                   o[4 * p + j + 1][nt][e] * inv, o[4 * p + j + 1][nt][2 + e] * inv);
+      }
+    }
   if (a.cluster > 1) cluster_sync_all();
   else __syncthreads();
+  // the prefix's partial sums are complete and visible from here on
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // Join: per row, the weights of every piece; warp w takes rows w, w + 4, ...
   const int pieces = kOwnWarps * a.cluster;
@@ -693,29 +749,53 @@ __global__ void __launch_bounds__(kOwnThreads)
       else
         own = sL[lane][row];
     }
+    float pre[kMaxRanges / 32];            // ranges lane, lane + 32 of the prefix
     float mx = own;
-    for (int i = lane; i < a.ns; i += 32) mx = fmaxf(mx, pl[static_cast<int64_t>(i) * a.R + row]);
+#pragma unroll
+    for (int i = 0; i < kMaxRanges / 32; ++i) {
+      const int rg = lane + 32 * i;
+      pre[i] = rg < a.ns ? __ldg(pl + static_cast<int64_t>(rg) * a.R + row) : -INFINITY;
+      mx = fmaxf(mx, pre[i]);
+    }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
     const float ms = mx == -INFINITY ? 0.f : mx;
     float sum = ex2(own - ms);
-    for (int i = lane; i < a.ns; i += 32) sum += ex2(pl[static_cast<int64_t>(i) * a.R + row] - ms);
+#pragma unroll
+    for (int i = 0; i < kMaxRanges / 32; ++i) sum += ex2(pre[i] - ms);
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
     const float L2 = mx == -INFINITY ? -INFINITY : ms + log2f(sum);
-    if (lane < pieces) sW[row][lane] = L2 == -INFINITY ? 0.f : ex2(own - L2);
-    if (lane == 0) sTot[row] = L2;
+    const float Lw = mx == -INFINITY ? 0.f : L2;
+    if (lane < pieces) sW[row][lane] = ex2(own - Lw);
+#pragma unroll
+    for (int i = 0; i < kMaxRanges / 32; ++i)
+      if (lane + 32 * i < a.ns) sP[row][lane + 32 * i] = ex2(pre[i] - Lw);
+    if (lane == 0 && rank == 0) {
+      const int gr = r0 + row, hg = gr / a.Nq, tok = gr - hg * a.Nq;
+      a.lse[(static_cast<int64_t>(b) * a.Hq + hk * a.G + hg) * a.Nq + tok] = L2 * kLn2;
+    }
   }
   __syncthreads();
   const int units = a.dreal / 4;
   for (int idx = threadIdx.x + kOwnThreads * rank; idx < nr * units; idx += kOwnThreads * a.cluster) {
     const int row = idx / units, un = idx - row * units;
-    const float L2 = sTot[row];
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     auto add = [&](float w, const float4& x) {
       acc.x = fmaf(w, x.x, acc.x); acc.y = fmaf(w, x.y, acc.y);
       acc.z = fmaf(w, x.z, acc.z); acc.w = fmaf(w, x.w, acc.w);
     };
+    const float* po = a.part_o + (static_cast<int64_t>(hk) * a.ns * a.R + prow + row) * a.dreal + 4 * un;
+    const int64_t step = static_cast<int64_t>(a.R) * a.dreal;
+    int i = 0;
+    for (; i + 8 <= a.ns; i += 8) {          // eight loads in flight
+      float4 x[8];
+#pragma unroll
+      for (int t = 0; t < 8; ++t) x[t] = __ldg(reinterpret_cast<const float4*>(po + (i + t) * step));
+#pragma unroll
+      for (int t = 0; t < 8; ++t) add(sP[row][i + t], x[t]);
+    }
+    for (; i < a.ns; ++i) add(sP[row][i], __ldg(reinterpret_cast<const float4*>(po + i * step)));
     for (int rk = 0; rk < a.cluster; ++rk)
 #pragma unroll
       for (int w = 0; w < kOwnWarps; ++w) {
@@ -724,20 +804,13 @@ __global__ void __launch_bounds__(kOwnThreads)
                              : *reinterpret_cast<const float4*>(&sO[w][row][4 * un]);
         add(sW[row][rk * kOwnWarps + w], x);
       }
-    const float* po = a.part_o + (static_cast<int64_t>(hk) * a.ns * a.R + prow + row) * a.dreal + 4 * un;
-#pragma unroll 4
-    for (int i = 0; i < a.ns; ++i) {
-      const float w = ex2(pl[static_cast<int64_t>(i) * a.R + row] - L2);
-      add(w, *reinterpret_cast<const float4*>(po + static_cast<int64_t>(i) * a.R * a.dreal));
-    }
     const int gr = r0 + row, hg = gr / a.Nq, tok = gr - hg * a.Nq;
-    const int64_t h = hk * a.G + hg;
-    T* dst = static_cast<T*>(a.o) + b * a.so[0] + h * a.so[1] + tok * a.so[2] + 4 * un;
+    T* dst = static_cast<T*>(a.o) + b * a.so[0] + static_cast<int64_t>(hk * a.G + hg) * a.so[1] +
+             tok * a.so[2] + 4 * un;
     uint2 w2;
     w2.x = pack2<T>(acc.x, acc.y);
     w2.y = pack2<T>(acc.z, acc.w);
     *reinterpret_cast<uint2*>(dst) = w2;
-    if (un == 0) a.lse[(static_cast<int64_t>(b) * a.Hq + h) * a.Nq + tok] = L2 * kLn2;
   }
   // no block leaves while another still reads its shared memory
   if (a.cluster > 1) cluster_sync_all();
@@ -761,7 +834,7 @@ PrefixPlan make_plan(int64_t B, int64_t Hkv, int64_t GN, int64_t D, int64_t P) {
   const double per_tile = D > 64 ? 1.5 : 0.8, fixed = 5.0;      // microseconds
   const double join = static_cast<double>(R) * Hkv * D * 8 / 10e6;  // per range
   double best = 0;
-  const int64_t most = n < 64 ? n : 64;
+  const int64_t most = n < kMaxRanges ? n : kMaxRanges;
   for (int64_t ns = 1; ns <= most; ++ns) {
     const double waves = static_cast<double>((base * ns + kPlanSMs - 1) / kPlanSMs);
     const double t = waves * (fixed + per_tile * static_cast<double>((n + ns - 1) / ns)) + join * ns;
@@ -814,19 +887,19 @@ fa_status run_decode(const DecodeParams& p, cudaStream_t stream) {
   a.S = p.S;
   a.B = static_cast<int>(p.B); a.Hq = static_cast<int>(p.Hkv * p.G); a.Hkv = static_cast<int>(p.Hkv);
   a.G = static_cast<int>(p.G); a.Nq = static_cast<int>(p.Nq); a.GN = static_cast<int>(GN);
-  a.RT = static_cast<int>((GN + 15) / 16);
+  const int NT = GN <= 8 ? 1 : 2;
+  a.RT = static_cast<int>((GN + 8 * NT - 1) / (8 * NT));
   a.dreal = static_cast<int>(p.D); a.causal = p.causal;
   a.c = p.scale * kLog2e;
   a.ns = pl.ns; a.R = static_cast<int>(R);
   a.part_o = part_o; a.part_l = part_l;
   a.status = p.status;
   const int64_t base = p.B * p.Hkv * a.RT;
-  // blocks of a cluster: enough to fill the SMs four times over, but each warp
+  // blocks of a cluster: as many as stay resident together, while each warp
   // keeps at least two blocks of 16 keys of the longest request allowed
+  const int64_t slots = static_cast<int64_t>(device_sm_count()) * own_blocks(D, NT);
   int cl = 1;
-  while (cl < kMaxCluster && base * cl < 4 * static_cast<int64_t>(device_sm_count()) &&
-         p.S >= 2 * 16 * kOwnWarps * 2 * cl)
-    cl *= 2;
+  while (cl < kMaxCluster && 2 * base * cl <= slots && p.S >= 2 * 16 * kOwnWarps * 2 * cl) cl *= 2;
   a.cluster = cl;
   const int64_t blocks = base * cl;
   if (blocks > 0x7fffffffLL) return FA_ERR_SHAPE;
@@ -834,16 +907,27 @@ fa_status run_decode(const DecodeParams& p, cudaStream_t stream) {
   cfg.gridDim = dim3(static_cast<unsigned>(blocks));
   cfg.blockDim = dim3(kOwnThreads);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
+  cfg.attrs = attr;
+  cfg.numAttrs = 0;
   if (cl > 1) {
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(cl);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cudaLaunchAttribute& at = attr[cfg.numAttrs++];
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = static_cast<unsigned>(cl);
+    at.val.clusterDim.y = 1;
+    at.val.clusterDim.z = 1;
   }
-  if (cudaLaunchKernelEx(&cfg, own_kernel<T, D>, a) != cudaSuccess) return FA_ERR_LAUNCH;
+  if (pl.ns > 0) {
+    // The own rows need nothing of the prefix kernel until the join, where
+    // every block waits for it (griddepcontrol.wait): its blocks start on SMs
+    // that the prefix kernel has left.  Without that kernel before it the
+    // launch is an ordinary one.
+    cudaLaunchAttribute& at = attr[cfg.numAttrs++];
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+  }
+  auto kern = NT == 1 ? own_kernel<T, D, 1> : own_kernel<T, D, 2>;
+  if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) return FA_ERR_LAUNCH;
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
