@@ -313,6 +313,17 @@ int device_sm_count() {
   return sms > 0 ? sms : 1;
 }
 
+bool configure_smem(const void* kernel, int bytes, std::atomic<uint64_t>* done) {
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return false;
+  const uint64_t bit = 1ull << dev;
+  if (done->load(std::memory_order_relaxed) & bit) return true;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+    return false;
+  done->fetch_or(bit, std::memory_order_relaxed);
+  return true;
+}
+
 // Side stream of each device, for a kernel that may overlap the caller's
 // stream (the backward's dQ kernel beside its dK/dV kernel).  One fork/join
 // at a time per device: the lock is held from side_begin to side_end, so two
@@ -616,9 +627,8 @@ static fa_status check_rotary(const fa_rotary* r, RotaryParams* out) {
     if (r->pos_stride[i] < 0) return FA_ERR_STRIDE;
   if ((r->q_weight != nullptr) != (r->k_weight != nullptr)) return FA_ERR_NULL;
   if (r->q_weight) {
-    const uintptr_t wa = r->weight_f32 || r->dtype == FA_F32 ? 4 : 2;
-    if (reinterpret_cast<uintptr_t>(r->q_weight) % wa != 0 ||
-        reinterpret_cast<uintptr_t>(r->k_weight) % wa != 0)
+    if (reinterpret_cast<uintptr_t>(r->q_weight) % 16 != 0 ||
+        reinterpret_cast<uintptr_t>(r->k_weight) % 16 != 0)
       return FA_ERR_ALIGN;
     if (!(std::isfinite(r->eps) && r->eps >= 0.f)) return FA_ERR_ARG;
   }
@@ -658,7 +668,7 @@ fa_status fa_rotary_fwd(const fa_rotary* rot, const void* q, const int64_t* sq, 
 size_t fa_rotary_bwd_workspace_bytes(const fa_rotary* rot) {
   RotaryParams p{};
   if (check_rotary(rot, &p) != FA_OK || !p.w[0]) return 0;
-  return static_cast<size_t>(kRotaryMaxParts) * 2 * static_cast<size_t>(p.D) * sizeof(float);
+  return static_cast<size_t>(kRotaryMaxParts) * static_cast<size_t>(p.D) * sizeof(float);
 }
 
 fa_status fa_rotary_bwd(const fa_rotary* rot, const void* q, const int64_t* sq, const void* k,

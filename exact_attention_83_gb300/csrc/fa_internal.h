@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 #include <cuda_fp16.h>
 #include <cuda_bf16.h>
+#include <atomic>
 #include <cstdint>
 
 #include "../../include/fa.h"
@@ -239,11 +240,11 @@ struct RotaryParams {
   float eps;
   int backward;
   float* dw[2];
-  float* ws;                 // kRotaryMaxParts * 2 * D floats
+  float* ws;                 // kRotaryMaxParts * D floats
 };
-// Blocks of the norm's gradient, each of which leaves one partial row of the
-// weight gradients: three per SM.
-constexpr int kRotaryMaxParts = 456;
+// Blocks of the norm's gradient at most, each of which leaves one partial row
+// of a weight's gradient: two per SM.
+constexpr int kRotaryMaxParts = 304;
 fa_status launch_rotary(const RotaryParams& p, cudaStream_t s);
 
 // Parameters of one fa_decode call.
@@ -306,6 +307,17 @@ bool encode_f32_rows_map(CUtensorMap* map, const float* base, int64_t cols, int6
 
 // Number of SMs of the current device (cached per device).
 int device_sm_count();
+
+// Raises a kernel's limit of dynamic shared memory once per device: the call
+// costs as much host time as a small kernel runs.  `done` is the kernel's own
+// record, a bit per device.
+bool configure_smem(const void* kernel, int bytes, std::atomic<uint64_t>* done);
+#define FA_CONFIGURE(kernel, bytes)                                                     \
+  do {                                                                                  \
+    static std::atomic<uint64_t> done_{0};                                              \
+    if (!configure_smem(reinterpret_cast<const void*>(&kernel), bytes, &done_))         \
+      return FA_ERR_LAUNCH;                                                             \
+  } while (0)
 
 // fa_bwd with the choice of letting the tensor-core dQ kernel use the side
 // stream (fa_bwd: yes; fa_bwd_noalloc, which creates nothing: no).

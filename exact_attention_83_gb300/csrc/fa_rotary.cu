@@ -23,20 +23,33 @@
 // What bounds it: HBM.  Each row is read once and written once (the gradient
 // of the norm reads two rows and writes one); the arithmetic is a few
 // operations per element.  So each lane owns 16 elements of a row as two
-// 16-byte units whose pairs it holds whole (units 8c and pairs + 8c for split
-// halves, 32 contiguous bytes for neighbouring pairs): no exchange between
-// lanes but the norm's sums.  A block takes a tile of tokens with all their
+// 8-element units whose pairs it holds whole (elements 8c and pairs + 8c for
+// split halves, 8c and D/2 + 8c for neighbouring pairs): no exchange between
+// lanes but the norm's sums, and neighbouring lanes touch neighbouring units.  A block takes a tile of tokens with all their
 // heads, so that the cosines and sines of a token are computed once, into
-// shared memory, for all its heads.
+// shared memory, for all its heads; a lane then keeps those of its pairs, and
+// its weights, in registers while it walks the heads.  Arithmetic is on pairs
+// of fp32, which halves its instructions, and rows are copied into shared
+// memory three or four steps ahead of the work (cp.async).
 
-#include "fa_internal.h"
+#include "tc_common.cuh"
 
 namespace fa {
 namespace {
 
+using tc::pack2;
+
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kMaxTile = 8;     // tokens per tile, at most
+// Tokens per tile at most: the angles of a tile take 8 KB.
+template <int D> constexpr int kMaxTile = 2048 / D;
+constexpr int kMostTokens = 128;
+
+// The tiles of a walk: tokens per tile, tiles per batch entry, tiles in all.
+struct Tiles {
+  int tok;
+  int64_t per, items;
+};
 
 struct RotArgs {
   const void* x[2];             // q, k (gradient: the incoming gradients)
@@ -45,10 +58,8 @@ struct RotArgs {
   int64_t sx[2][3], sin[2][3], so[2][3];   // element strides (b, h, n)
   int64_t N;
   int heads[2];
-  int h_fast[2];                // consecutive rows of a tile: heads of a token, or tokens of a head
-  int tile, tiles;              // tokens per tile, tiles per batch entry
-  int64_t items;                // B * tiles
-  int pairs, interleaved, naxes;
+  Tiles tiles[2];               // forward: [0]; gradient of the norm: of q and of k
+  int pairs, naxes;
   int sec_end[4];               // first pair past each axis
   const float* inv_freq;
   const void* pos;
@@ -57,38 +68,63 @@ struct RotArgs {
   const void* w[2];
   int w_f32;
   float eps, sign;              // sign: +1 forward, -1 gradient
-  float* dw_part;               // [grid][2][D] partial weight gradients
+  int split;                    // gradient of the norm: blocks that work on q
+  float* dw_part;               // [grid][D] partial weight gradients
 };
 
 // ------------------------------------------------------------------ row access
-template <typename T> struct Unit;      // 8 consecutive elements
-template <> struct Unit<float> {
-  static __device__ __forceinline__ void load(const float* p, float (&v)[8]) {
-    const float4 a = __ldcs(reinterpret_cast<const float4*>(p));
-    const float4 b = __ldcs(reinterpret_cast<const float4*>(p) + 1);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-  }
-  static __device__ __forceinline__ void store(float* p, const float (&v)[8]) {
-    __stcs(reinterpret_cast<float4*>(p), make_float4(v[0], v[1], v[2], v[3]));
-    __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(v[4], v[5], v[6], v[7]));
-  }
-};
-template <typename T> struct Unit {
-  static __device__ __forceinline__ void load(const T* p, float (&v)[8]) {
-    const uint4 u = __ldcs(reinterpret_cast<const uint4*>(p));
-    const T* e = reinterpret_cast<const T*>(&u);
+// A lane's unit of a row is eight consecutive elements, taken as four pairs of
+// fp32.  Units travel through a ring in shared memory (cp.async), a few rows
+// ahead of the work and without registers; a thread copies and reads its own
+// 16-byte pieces only, so the ring needs no barrier.
+template <typename T> constexpr int kPieces = sizeof(T) == 2 ? 1 : 2;   // 16-byte pieces of a unit
+
+template <typename T>
+__device__ __forceinline__ void copy_unit(uint4* slot, const T* p) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = Elem<T>::to_f32(e[i]);
-  }
-  static __device__ __forceinline__ void store(T* p, const float (&v)[8]) {
-    uint4 u;
-    T* e = reinterpret_cast<T*>(&u);
+  for (int i = 0; i < kPieces<T>; ++i)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_u32(slot + i * kThreads)),
+                 "l"(reinterpret_cast<const uint4*>(p) + i)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+template <typename T>
+__device__ __forceinline__ void unpack16(const uint4& u, float2 (&x)[4]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) e[i] = Elem<T>::from_f32(v[i]);
-    __stcs(reinterpret_cast<uint4*>(p), u);
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (std::is_same<T, __nv_bfloat16>::value)
+      x[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    else
+      x[i] = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
   }
-};
+}
+__device__ __forceinline__ void unpack32(const uint4& u, const uint4& v, float2 (&x)[4]) {
+  x[0] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
+  x[1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
+  x[2] = make_float2(__uint_as_float(v.x), __uint_as_float(v.y));
+  x[3] = make_float2(__uint_as_float(v.z), __uint_as_float(v.w));
+}
+template <typename T>
+__device__ __forceinline__ void read_unit(const uint4* slot, float2 (&x)[4]) {
+  if constexpr (sizeof(T) == 2) unpack16<T>(slot[0], x);
+  else unpack32(slot[0], slot[kThreads], x);
+}
+template <typename T>
+__device__ __forceinline__ void store_unit(T* p, const float2 (&x)[4]) {
+  if constexpr (sizeof(T) == 4) {
+    __stcs(reinterpret_cast<float4*>(p), make_float4(x[0].x, x[0].y, x[1].x, x[1].y));
+    __stcs(reinterpret_cast<float4*>(p) + 1, make_float4(x[2].x, x[2].y, x[3].x, x[3].y));
+  } else {
+    __stcs(reinterpret_cast<uint4*>(p), make_uint4(pack2<T>(x[0].x, x[0].y), pack2<T>(x[1].x, x[1].y),
+                                                   pack2<T>(x[2].x, x[2].y), pack2<T>(x[3].x, x[3].y)));
+  }
+}
 
 // ---------------------------------------------------------------------- angles
 // frac(f / 2 pi) * 2^64 for a finite fp32 f: the 24-bit significand times the
@@ -118,277 +154,559 @@ __device__ __forceinline__ uint64_t turns_per_position(float f) {
   return (bits >> 31) ? 0 - r : r;
 }
 
-// Cosines and sines of a tile's tokens: cs[token][pair].
-__device__ __forceinline__ void angle_table(const RotArgs& a, float2* cs, int64_t b, int64_t n0,
-                                            int ntok) {
-  const int total = ntok * a.pairs;
-  for (int idx = threadIdx.x; idx < total; idx += kThreads) {
-    const int tok = idx / a.pairs, i = idx - tok * a.pairs;
+// Per block: each pair's turns per position and its axis, and a tile's positions.
+struct PairTable {
+  uint64_t turns[64];
+  int64_t pos[2][4][kMostTokens];   // of the tile at work and the next
+  uint8_t axis[64];
+};
+__device__ __forceinline__ void pair_table(const RotArgs& a, PairTable& t) {
+  for (int i = threadIdx.x; i < a.pairs; i += kThreads) {
+    t.turns[i] = turns_per_position(__ldg(a.inv_freq + i));
     int ax = 0;
 #pragma unroll
     for (int s = 0; s < 3; ++s)
       if (s + 1 < a.naxes && i >= a.sec_end[s]) ax = s + 1;
+    t.axis[i] = static_cast<uint8_t>(ax);
+  }
+}
+// The positions of tile `item` (nothing past the last one), into buffer `buf`.
+__device__ __forceinline__ void tile_positions(const RotArgs& a, const Tiles& tl, PairTable& t,
+                                               int64_t item, int buf) {
+  if (item >= tl.items) return;
+  const int64_t b = item / tl.per, n0 = (item - b * tl.per) * tl.tok;
+  // from the last thread down: pair_table keeps the first ones busy
+  for (int i = kThreads - 1 - static_cast<int>(threadIdx.x); i < a.naxes * tl.tok; i += kThreads) {
+    const int ax = i / tl.tok, tok = i - ax * tl.tok;
+    if (n0 + tok >= a.N) continue;
     const int64_t at = ax * a.ps[0] + b * a.ps[1] + (n0 + tok) * a.ps[2];
-    const int64_t p = a.pos64 ? __ldg(static_cast<const long long*>(a.pos) + at)
-                              : static_cast<int64_t>(__ldg(static_cast<const int*>(a.pos) + at));
-    const uint64_t turn = static_cast<uint64_t>(p) * turns_per_position(__ldg(a.inv_freq + i));
+    t.pos[buf][ax][tok] = a.pos64 ? __ldg(static_cast<const long long*>(a.pos) + at)
+                                  : static_cast<int64_t>(__ldg(static_cast<const int*>(a.pos) + at));
+  }
+}
+
+// Where the cosine of pair i of a token lies in its table of D floats (the sine
+// 4 LPR floats on), so that the lanes of a row read 16-byte pieces that are
+// neighbours: cosines of a lane's first four pairs, their sines, cosines of its
+// last four, their sines, piece j of lane c at float 4 (j LPR + c).  Lane c's
+// pairs are 8c .. 8c+7, or, with neighbouring pairs (IL), the four of unit c
+// and the four of unit LPR + c.
+template <int LPR, bool IL>
+__device__ __forceinline__ int cos_at(int i) {
+  const int unit = i >> 2;
+  const int c = IL ? unit % LPR : unit >> 1, half = IL ? unit / LPR : unit & 1;
+  return 4 * (2 * half * LPR + c) + (i & 3);
+}
+
+// Cosines and sines of a tile's tokens (cos_at), from the positions in buffer
+// `buf`.  Tokens past the end get angles of
+// whatever the buffer holds, which nobody uses.
+template <int D, bool IL>
+__device__ __forceinline__ void angle_table(const RotArgs& a, const PairTable& pt, float* cs, int tile,
+                                            int buf) {
+  constexpr int LPR = D / 16;
+  const int total = tile * a.pairs;
+  for (int idx = threadIdx.x; idx < total; idx += kThreads) {
+    const int tok = idx / a.pairs, i = idx - tok * a.pairs;
+    const uint64_t turn = static_cast<uint64_t>(pt.pos[buf][pt.axis[i]][tok]) * pt.turns[i];
     // top 32 bits as a signed fraction: half turns in [-1, 1)
     const float half = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f;
     float s, c;
     sincospif(half, &s, &c);
-    cs[idx] = make_float2(c, a.sign * s);
+    float* dst = cs + tok * D + cos_at<LPR, IL>(i);
+    dst[0] = c;
+    dst[4 * LPR] = a.sign * s;
   }
 }
 
-// Where a lane's two units of a row lie, and its first pair (or -1: elements
-// past the rotated ones).
+// Where a lane's two units of a row lie, and whether their pairs are rotated.
 struct LaneUnits {
-  int off_a, off_b, pair;
+  int off_a, off_b;
+  bool rot_a, rot_b;
 };
-__device__ __forceinline__ LaneUnits lane_units(int c, int pairs, int interleaved) {
+template <int LPR, bool IL>
+__device__ __forceinline__ LaneUnits lane_units(int c, int pairs) {
   LaneUnits u;
-  const int rc = pairs / 8;                      // lanes that hold rotated pairs
-  u.pair = c < rc ? 8 * c : -1;
-  if (c >= rc || interleaved) {
-    u.off_a = 16 * c;
-    u.off_b = 16 * c + 8;
-  } else {
+  if constexpr (IL) {
     u.off_a = 8 * c;
-    u.off_b = pairs + 8 * c;
+    u.off_b = 8 * (LPR + c);
+    u.rot_a = 4 * c < pairs;
+    u.rot_b = 4 * (LPR + c) < pairs;
+  } else {
+    const int rc = pairs / 8;                    // lanes that hold rotated pairs
+    u.rot_a = u.rot_b = c < rc;
+    u.off_a = c < rc ? 8 * c : 2 * pairs + 8 * (c - rc);
+    u.off_b = c < rc ? pairs + 8 * c : 2 * pairs + 8 * (LPR - rc + c - rc);
   }
   return u;
 }
 
-// Rotates a lane's 16 elements in place by the tabled angles.
-__device__ __forceinline__ void rotate(float (&va)[8], float (&vb)[8], const float2* cs,
-                                       bool interleaved) {
-  float c[8], s[8];
+// A lane's eight cosines and sines (identity where nothing is rotated).
+struct Angles {
+  float2 c[4], s[4];
+};
+template <int LPR>
+__device__ __forceinline__ void load_angles(const float* cs_tok, int c, const LaneUnits& u, Angles& g) {
 #pragma unroll
-  for (int i = 0; i < 8; i += 2) {
-    const float4 t = *reinterpret_cast<const float4*>(cs + i);
-    c[i] = t.x; s[i] = t.y; c[i + 1] = t.z; s[i + 1] = t.w;
+  for (int j = 0; j < 2; ++j) {
+    float4 x = make_float4(1.f, 1.f, 1.f, 1.f), y = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (j ? u.rot_b : u.rot_a) {
+      x = *reinterpret_cast<const float4*>(cs_tok + 4 * (2 * j * LPR + c));
+      y = *reinterpret_cast<const float4*>(cs_tok + 4 * ((2 * j + 1) * LPR + c));
+    }
+    g.c[2 * j] = make_float2(x.x, x.y);
+    g.c[2 * j + 1] = make_float2(x.z, x.w);
+    g.s[2 * j] = make_float2(y.x, y.y);
+    g.s[2 * j + 1] = make_float2(y.z, y.w);
   }
-  if (interleaved) {
+}
+
+// The rotation of a lane's 16 elements as coefficients: a' = a ca + b sb,
+// b' = a sa + b cb for each of the eight pairs.  A norm's weights are folded
+// in: ca = w_a cos, sb = -w_b sin, sa = w_a sin, cb = w_b cos.  Split halves
+// hold pairs 2i, 2i + 1 in element pair i of each unit; with neighbouring pairs
+// (IL) element pair i of the first unit is pair i, of the second pair 4 + i.
+struct Turn {
+  float2 ca[4], sb[4], sa[4], cb[4];
+};
+__device__ __forceinline__ float2 neg(float2 x) { return make_float2(-x.x, -x.y); }
+template <bool IL>
+__device__ __forceinline__ void make_turn(const Angles& g, Turn& t) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float x0 = va[2 * i], y0 = va[2 * i + 1], x1 = vb[2 * i], y1 = vb[2 * i + 1];
-      va[2 * i] = x0 * c[i] - y0 * s[i];
-      va[2 * i + 1] = x0 * s[i] + y0 * c[i];
-      vb[2 * i] = x1 * c[4 + i] - y1 * s[4 + i];
-      vb[2 * i + 1] = x1 * s[4 + i] + y1 * c[4 + i];
+  for (int i = 0; i < 4; ++i) {
+    t.ca[i] = t.cb[i] = g.c[i];
+    t.sa[i] = g.s[i];
+    t.sb[i] = neg(g.s[i]);
+  }
+}
+template <bool IL>
+__device__ __forceinline__ void make_turn(const Angles& g, const float2 (&wa)[4], const float2 (&wb)[4],
+                                          Turn& t) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float2 a, b;                         // weights of a's and b's of pairs 2i, 2i + 1
+    if constexpr (IL) {
+      const float2 e0 = i < 2 ? wa[2 * i] : wb[2 * i - 4], e1 = i < 2 ? wa[2 * i + 1] : wb[2 * i - 3];
+      a = make_float2(e0.x, e1.x);
+      b = make_float2(e0.y, e1.y);
+    } else {
+      a = wa[i];
+      b = wb[i];
+    }
+    t.ca[i] = __fmul2_rn(a, g.c[i]);
+    t.sa[i] = __fmul2_rn(a, g.s[i]);
+    t.cb[i] = __fmul2_rn(b, g.c[i]);
+    t.sb[i] = neg(__fmul2_rn(b, g.s[i]));
+  }
+}
+template <bool IL>
+__device__ __forceinline__ void turn(float2 (&va)[4], float2 (&vb)[4], const Turn& t) {
+  if constexpr (IL) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float2& v = i < 4 ? va[i & 3] : vb[i & 3];
+      const float ca = i & 1 ? t.ca[i >> 1].y : t.ca[i >> 1].x, sb = i & 1 ? t.sb[i >> 1].y : t.sb[i >> 1].x;
+      const float sa = i & 1 ? t.sa[i >> 1].y : t.sa[i >> 1].x, cb = i & 1 ? t.cb[i >> 1].y : t.cb[i >> 1].x;
+      v = make_float2(fmaf(v.x, ca, v.y * sb), fmaf(v.x, sa, v.y * cb));
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float x = va[i], y = vb[i];
-      va[i] = x * c[i] - y * s[i];
-      vb[i] = x * s[i] + y * c[i];
+    for (int i = 0; i < 4; ++i) {
+      const float2 x = va[i], y = vb[i];
+      va[i] = __ffma2_rn(x, t.ca[i], __fmul2_rn(y, t.sb[i]));
+      vb[i] = __ffma2_rn(x, t.sa[i], __fmul2_rn(y, t.cb[i]));
     }
   }
 }
 
 template <int LPR>
-__device__ __forceinline__ float row_sum(float v) {
+__device__ __forceinline__ float row_sum(float2 v2) {
+  float v = v2.x + v2.y;
 #pragma unroll
   for (int o = LPR / 2; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
 
-// Row r of a tile's rows of tensor t (q or k): its token and head.
-__device__ __forceinline__ void tile_row(const RotArgs& a, int t, int r, int ntok, int& tok, int& h) {
-  if (a.h_fast[t]) {
-    tok = r / a.heads[t];
-    h = r - tok * a.heads[t];
+// Which rows of a tile a warp takes.  A warp holds RPW rows at a time: `tpw`
+// tokens (a power of two, as many as the tile has) with RPW / tpw heads each.
+// The tile's token groups are dealt to the warps (a tile has at most kWarps of
+// them); the warps left over share the heads of a group.  So a lane works on
+// one token of a tile and walks its heads.
+struct WarpRows {
+  int tok;         // this lane's token within the tile
+  int h0, step;    // its first head, and the distance to the next
+  int first;       // the warp's first head
+};
+template <int RPW>
+__device__ __forceinline__ WarpRows warp_rows(int tile, int warp, int sub) {
+  const int tpw = RPW < tile ? RPW : tile, hpi = RPW / tpw, groups = tile / tpw;
+  WarpRows r;
+  r.tok = (warp % groups) * tpw + sub / hpi;
+  r.first = (warp / groups) * hpi;
+  r.h0 = r.first + sub % hpi;
+  r.step = (kWarps / groups) * hpi;
+  return r;
+}
+// Heads h0, h0 + step, ... below `heads`.
+__device__ __forceinline__ int head_steps(int heads, int h0, int step) {
+  return h0 < heads ? (heads - h0 + step - 1) / step : 0;
+}
+
+// A tensor's norm weights of a lane's 16 elements.
+template <typename T>
+__device__ __forceinline__ void load_weights(const RotArgs& a, int t, const LaneUnits& u,
+                                             float2 (&wa)[4], float2 (&wb)[4]) {
+  if (sizeof(T) == 4 || a.w_f32) {
+    const float* w = static_cast<const float*>(a.w[t]);
+    const uint4* pa = reinterpret_cast<const uint4*>(w + u.off_a);
+    const uint4* pb = reinterpret_cast<const uint4*>(w + u.off_b);
+    unpack32(__ldg(pa), __ldg(pa + 1), wa);
+    unpack32(__ldg(pb), __ldg(pb + 1), wb);
   } else {
-    h = r / ntok;
-    tok = r - h * ntok;
+    if constexpr (sizeof(T) == 2) {
+      const T* w = static_cast<const T*>(a.w[t]);
+      unpack16<T>(__ldg(reinterpret_cast<const uint4*>(w + u.off_a)), wa);
+      unpack16<T>(__ldg(reinterpret_cast<const uint4*>(w + u.off_b)), wb);
+    }
   }
 }
 
-template <int D>
-__device__ __forceinline__ void load_weights(const RotArgs& a, float* sw, bool half_type, bool bf16) {
-  for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
-    const void* w = a.w[i / D];
-    const int d = i % D;
-    float v;
-    if (a.w_f32 || !half_type) v = static_cast<const float*>(w)[d];
-    else if (bf16) v = __bfloat162float(static_cast<const __nv_bfloat16*>(w)[d]);
-    else v = __half2float(static_cast<const __half*>(w)[d]);
-    sw[i] = v;
-  }
-}
-
+// Blocks per SM that the registers are kept to, and rows of the ring.
 template <typename T>
-constexpr bool kHalf = sizeof(T) == 2;
-template <typename T>
-constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+constexpr int fwd_blocks(bool norm) { return !norm && sizeof(T) == 2 ? 3 : 2; }
+constexpr int kBwdBlocks = 2;
+template <typename T> constexpr int kFwdRing = sizeof(T) == 2 ? 5 : 3;
+template <typename T> constexpr int kBwdRing = sizeof(T) == 2 ? 4 : 2;
+template <typename T> constexpr int kFwdSmem = kFwdRing<T> * 2 * kPieces<T> * kThreads * 16;
+template <typename T> constexpr int kBwdSmem = kBwdRing<T> * 4 * kPieces<T> * kThreads * 16;
 
-template <typename T, int D, bool NORM>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotArgs a) {
+// Both kernels walk tiles.  While a tile's rows are worked on, the rows of the
+// steps to come (over the ends of tiles) are being copied, the next tile's
+// angles are formed into the other half of the table and the positions of the
+// tile after it are read: one barrier per tile, and no wait for memory at its
+// start.
+template <typename T, int D, bool NORM, bool IL>
+__global__ void __launch_bounds__(kThreads, fwd_blocks<T>(NORM)) rotary_kernel(const __grid_constant__ RotArgs a) {
   constexpr int LPR = D / 16;            // lanes per row
   constexpr int RPW = 32 / LPR;          // rows per warp
-  __shared__ __align__(16) float2 cs[kMaxTile * (D / 2)];
-  __shared__ __align__(16) float sw[NORM ? 2 * D : 4];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const LaneUnits u = lane_units(lane % LPR, a.pairs, a.interleaved);
-  if constexpr (NORM) load_weights<D>(a, sw, kHalf<T>, kBf16<T>);
-  const int64_t b = blockIdx.x / a.tiles, n0 = static_cast<int64_t>(blockIdx.x % a.tiles) * a.tile;
-  const int ntok = static_cast<int>(a.N - n0 < a.tile ? a.N - n0 : a.tile);
-  angle_table(a, cs, b, n0, ntok);
-  __syncthreads();
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const T* x = static_cast<const T*>(a.x[t]) + b * a.sx[t][0] + n0 * a.sx[t][2];
-    T* out = static_cast<T*>(a.out[t]) + b * a.so[t][0] + n0 * a.so[t][2];
-    const int rows = ntok * a.heads[t];
-    // whole warps stay in the loop: the norm's sums are exchanged
-    for (int r0 = warp * RPW; r0 < rows; r0 += kWarps * RPW) {
-      const int r = r0 + lane / LPR;
-      const bool on = r < rows;
-      int tok, h;
-      tile_row(a, t, on ? r : 0, ntok, tok, h);
-      float va[8], vb[8];
-      const T* row = x + h * a.sx[t][1] + tok * a.sx[t][2];
-      Unit<T>::load(row + u.off_a, va);
-      Unit<T>::load(row + u.off_b, vb);
-      if constexpr (NORM) {
-        float ss = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss = fmaf(va[i], va[i], fmaf(vb[i], vb[i], ss));
-        const float rstd = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + a.eps);
-        const float* w = sw + t * D;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          va[i] *= rstd * w[u.off_a + i];
-          vb[i] *= rstd * w[u.off_b + i];
-        }
+  constexpr int S = kFwdRing<T>, U = kPieces<T> * kThreads;    // pieces of a unit of all threads
+  extern __shared__ __align__(16) uint4 ring[];                 // [S][a | b][pieces][thread]
+  __shared__ __align__(16) float cs[2][kMaxTile<D> * D];
+  __shared__ PairTable pt;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % LPR;
+  const LaneUnits u = lane_units<LPR, IL>(c, a.pairs);
+  const int ab = u.off_b - u.off_a;
+  const Tiles& tl = a.tiles[0];
+  const WarpRows w = warp_rows<RPW>(tl.tok, warp, lane / LPR);
+  // steps of the warp on a tile, and those of them in which this lane has a row
+  const int it[2] = {head_steps(a.heads[0], w.first, w.step), head_steps(a.heads[1], w.first, w.step)};
+  const int mine_q = head_steps(a.heads[0], w.h0, w.step), mine_k = head_steps(a.heads[1], w.h0, w.step);
+
+  // The next step to copy: of q (p_t = 0) or k of tile p_item, p_seg steps left
+  // for the warp, p_left for this lane, at p_row.
+  int64_t p_item = static_cast<int64_t>(blockIdx.x) - gridDim.x;
+  int p_t = 1, p_seg = 0, p_left = 0, p_slot = 0;
+  int64_t p_n = 0, p_b = 0, p_step = 0;
+  const T* p_row = nullptr;
+  auto next_segment = [&]() {
+    do {
+      p_t ^= 1;
+      if (p_t == 0) {
+        p_item += gridDim.x;
+        if (p_item >= tl.items) return;
+        p_b = p_item / tl.per;
+        p_n = (p_item - p_b * tl.per) * tl.tok + w.tok;
       }
-      if (u.pair >= 0) rotate(va, vb, cs + tok * a.pairs + u.pair, a.interleaved);
-      if (on) {
-        T* dst = out + h * a.so[t][1] + tok * a.so[t][2];
-        Unit<T>::store(dst + u.off_a, va);
-        Unit<T>::store(dst + u.off_b, vb);
+      p_seg = p_t ? it[1] : it[0];
+      p_left = p_n < a.N ? (p_t ? mine_k : mine_q) : 0;
+      p_step = w.step * a.sx[p_t][1];
+      p_row = static_cast<const T*>(a.x[p_t]) + p_b * a.sx[p_t][0] + p_n * a.sx[p_t][2] +
+              w.h0 * a.sx[p_t][1] + u.off_a;
+    } while (p_seg == 0);
+  };
+  uint4* mine = ring + threadIdx.x;
+  auto issue = [&]() {
+    if (p_seg > 0) {
+      if (p_left > 0) {
+        uint4* slot = mine + p_slot * 2 * U;
+        copy_unit<T>(slot, p_row);
+        copy_unit<T>(slot + U, p_row + ab);
       }
+      p_slot = p_slot + 1 == S ? 0 : p_slot + 1;
+      p_row += p_step;
+      --p_left;
+      if (--p_seg == 0) next_segment();
     }
-  }
-}
-
-// Gradient of the norm with the rotation.  A block walks tiles and keeps its
-// lanes' sums of the weight gradients in registers (16 columns of each
-// tensor's weight per lane), joins them once at the end and leaves one partial
-// row per tensor; weight_grad_kernel adds the blocks' rows in a fixed order,
-// so the result does not depend on the schedule.
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) qk_norm_bwd_kernel(const __grid_constant__ RotArgs a) {
-  constexpr int LPR = D / 16, RPW = 32 / LPR;
-  __shared__ __align__(16) float2 cs[kMaxTile * (D / 2)];
-  __shared__ __align__(16) float sw[2 * D];
-  __shared__ float red[kWarps][D];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const LaneUnits u = lane_units(lane % LPR, a.pairs, a.interleaved);
-  load_weights<D>(a, sw, kHalf<T>, kBf16<T>);
-  float acc[2][16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) acc[0][i] = acc[1][i] = 0.f;
-
-  for (int64_t item = blockIdx.x; item < a.items; item += gridDim.x) {
-    const int64_t b = item / a.tiles, n0 = (item - b * a.tiles) * a.tile;
-    const int ntok = static_cast<int>(a.N - n0 < a.tile ? a.N - n0 : a.tile);
-    __syncthreads();                      // the last tile's table is no longer read
-    angle_table(a, cs, b, n0, ntok);
-    __syncthreads();
+    copy_commit();
+  };
+  if (it[0] + it[1] > 0) next_segment();   // a warp without heads copies nothing
+  for (int i = 0; i < S - 1; ++i) issue();
+  tile_positions(a, tl, pt, blockIdx.x, 0);
+  tile_positions(a, tl, pt, static_cast<int64_t>(blockIdx.x) + gridDim.x, 1);
+  pair_table(a, pt);
+  __syncthreads();
+  angle_table<D, IL>(a, pt, cs[0], tl.tok, 0);
+  __syncthreads();
+  int slot_i = 0, buf = 0;
+  for (int64_t item = blockIdx.x; item < tl.items; item += gridDim.x, buf ^= 1) {
+    const int64_t b = item / tl.per, n = (item - b * tl.per) * tl.tok + w.tok;
+    Angles g;
+    load_angles<LPR>(cs[buf] + w.tok * D, c, u, g);
+    Turn tn;
+    if constexpr (!NORM) make_turn<IL>(g, tn);
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      const T* g = static_cast<const T*>(a.x[t]) + b * a.sx[t][0] + n0 * a.sx[t][2];
-      const T* x = static_cast<const T*>(a.in[t]) + b * a.sin[t][0] + n0 * a.sin[t][2];
-      T* out = static_cast<T*>(a.out[t]) + b * a.so[t][0] + n0 * a.so[t][2];
-      const int rows = ntok * a.heads[t];
-      for (int r0 = warp * RPW; r0 < rows; r0 += kWarps * RPW) {
-        const int r = r0 + lane / LPR;
-        const bool on = r < rows;
-        int tok, h;
-        tile_row(a, t, on ? r : 0, ntok, tok, h);
-        float ga[8], gb[8], xa[8], xb[8];
-        const T* grow = g + h * a.sx[t][1] + tok * a.sx[t][2];
-        const T* xrow = x + h * a.sin[t][1] + tok * a.sin[t][2];
-        Unit<T>::load(grow + u.off_a, ga);
-        Unit<T>::load(grow + u.off_b, gb);
-        Unit<T>::load(xrow + u.off_a, xa);
-        Unit<T>::load(xrow + u.off_b, xb);
-        if (u.pair >= 0) rotate(ga, gb, cs + tok * a.pairs + u.pair, a.interleaved);
-        const float* w = sw + t * D;
-        float ss = 0.f, sg = 0.f;
+      if constexpr (NORM) {
+        float2 wa[4], wb[4];
+        load_weights<T>(a, t, u, wa, wb);
+        make_turn<IL>(g, wa, wb, tn);
+      }
+      int left = n < a.N ? (t ? mine_k : mine_q) : 0;
+      const int64_t step = w.step * a.so[t][1];
+      T* out = static_cast<T*>(a.out[t]) + b * a.so[t][0] + n * a.so[t][2] + w.h0 * a.so[t][1] + u.off_a;
+      // whole warps walk the steps: the norm's sums are exchanged
+      for (int j = it[t]; j > 0; --j, --left, out += step) {
+        float2 va[4], vb[4];
+        copy_wait<S - 2>();
+        const uint4* slot = mine + slot_i * 2 * U;
+        read_unit<T>(slot, va);
+        read_unit<T>(slot + U, vb);
+        slot_i = slot_i + 1 == S ? 0 : slot_i + 1;
+        issue();                         // into the slot that the last step read
+        if constexpr (NORM) {
+          float2 ss = __fmul2_rn(va[0], va[0]), st = __fmul2_rn(vb[0], vb[0]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          ss = fmaf(xa[i], xa[i], fmaf(xb[i], xb[i], ss));
-          sg = fmaf(ga[i] * w[u.off_a + i], xa[i], fmaf(gb[i] * w[u.off_b + i], xb[i], sg));
-        }
-        const float rstd = rsqrtf(row_sum<LPR>(ss) * (1.f / D) + a.eps);
-        // xhat mean(g w xhat) = x rstd^2 (sum g w x) / D
-        const float m = row_sum<LPR>(sg) * (1.f / D) * rstd * rstd;
-        const float rs = on ? rstd : 0.f;      // lanes without a row add nothing
+          for (int q = 1; q < 4; ++q) {
+            ss = __ffma2_rn(va[q], va[q], ss);
+            st = __ffma2_rn(vb[q], vb[q], st);
+          }
+          const float rstd = rsqrtf(row_sum<LPR>(__fadd2_rn(ss, st)) * (1.f / D) + a.eps);
+          const float2 r2 = make_float2(rstd, rstd);
+          turn<IL>(va, vb, tn);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          acc[t][i] = fmaf(ga[i] * xa[i], rs, acc[t][i]);
-          acc[t][8 + i] = fmaf(gb[i] * xb[i], rs, acc[t][8 + i]);
-          ga[i] = rstd * (ga[i] * w[u.off_a + i] - xa[i] * m);
-          gb[i] = rstd * (gb[i] * w[u.off_b + i] - xb[i] * m);
+          for (int q = 0; q < 4; ++q) {
+            va[q] = __fmul2_rn(va[q], r2);
+            vb[q] = __fmul2_rn(vb[q], r2);
+          }
+        } else {
+          turn<IL>(va, vb, tn);
         }
-        if (on) {
-          T* dst = out + h * a.so[t][1] + tok * a.so[t][2];
-          Unit<T>::store(dst + u.off_a, ga);
-          Unit<T>::store(dst + u.off_b, gb);
+        if (left > 0) {
+          store_unit<T>(out, va);
+          store_unit<T>(out + ab, vb);
         }
       }
     }
+    if (item + gridDim.x < tl.items) {
+      angle_table<D, IL>(a, pt, cs[buf ^ 1], tl.tok, buf ^ 1);
+      tile_positions(a, tl, pt, item + 2 * static_cast<int64_t>(gridDim.x), buf);
+      __syncthreads();
+    }
   }
+  copy_wait<0>();
+}
+
+// Gradient of the norm with the rotation.  A block works on one tensor
+// (blocks below `split` on q, the others on k), walks that tensor's tiles and
+// keeps its lanes' sums of the weight gradient in registers (16 columns per
+// lane), joins them once at the end and leaves one partial row;
+// weight_grad_kernel adds the blocks' rows in a fixed order, so the result does
+// not depend on the schedule.
+template <typename T, int D, bool IL>
+__global__ void __launch_bounds__(kThreads, kBwdBlocks) qk_norm_bwd_kernel(const __grid_constant__ RotArgs a) {
+  constexpr int LPR = D / 16, RPW = 32 / LPR;
+  constexpr int S = kBwdRing<T>, U = kPieces<T> * kThreads;
+  extern __shared__ __align__(16) uint4 ring[];                 // [S][ga | gb | xa | xb][pieces][thread]
+  __shared__ __align__(16) float cs[2][kMaxTile<D> * D];
+  __shared__ PairTable pt;
+  __shared__ float red[kWarps][D];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % LPR;
+  const LaneUnits u = lane_units<LPR, IL>(c, a.pairs);
+  const int ab = u.off_b - u.off_a;
+  const int t = static_cast<int>(blockIdx.x) >= a.split ? 1 : 0;
+  const int blk = static_cast<int>(blockIdx.x) - (t ? a.split : 0);
+  const int nblk = t ? static_cast<int>(gridDim.x) - a.split : a.split;
+  const Tiles tl = a.tiles[t];
+  const WarpRows w = warp_rows<RPW>(tl.tok, warp, lane / LPR);
+  const int iters = head_steps(a.heads[t], w.first, w.step), mine_h = head_steps(a.heads[t], w.h0, w.step);
+  const int64_t sg = w.step * a.sx[t][1], sx = w.step * a.sin[t][1], so = w.step * a.so[t][1];
+  float2 wa[4], wb[4], acc_a[4], acc_b[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) acc_a[i] = acc_b[i] = make_float2(0.f, 0.f);
+
+  // the next step to copy: of tile p_item, p_seg steps left for the warp, p_left
+  // for this lane, rows p_g and p_x
+  int64_t p_item = static_cast<int64_t>(blk) - nblk;
+  int p_seg = 0, p_left = 0, p_slot = 0;
+  const T *p_g = nullptr, *p_x = nullptr;
+  auto next_tile = [&]() {
+    p_item += nblk;
+    if (p_item >= tl.items) return;
+    const int64_t b = p_item / tl.per, n = (p_item - b * tl.per) * tl.tok + w.tok;
+    p_seg = iters;
+    p_left = n < a.N ? mine_h : 0;
+    p_g = static_cast<const T*>(a.x[t]) + b * a.sx[t][0] + n * a.sx[t][2] + w.h0 * a.sx[t][1] + u.off_a;
+    p_x = static_cast<const T*>(a.in[t]) + b * a.sin[t][0] + n * a.sin[t][2] + w.h0 * a.sin[t][1] + u.off_a;
+  };
+  uint4* mine = ring + threadIdx.x;
+  auto issue = [&]() {
+    if (p_seg > 0) {
+      if (p_left > 0) {
+        uint4* slot = mine + p_slot * 4 * U;
+        copy_unit<T>(slot, p_g);
+        copy_unit<T>(slot + U, p_g + ab);
+        copy_unit<T>(slot + 2 * U, p_x);
+        copy_unit<T>(slot + 3 * U, p_x + ab);
+      }
+      p_slot = p_slot + 1 == S ? 0 : p_slot + 1;
+      p_g += sg;
+      p_x += sx;
+      --p_left;
+      if (--p_seg == 0) next_tile();
+    }
+    copy_commit();
+  };
+  next_tile();
+  for (int i = 0; i < S - 1; ++i) issue();
+  load_weights<T>(a, t, u, wa, wb);
+  tile_positions(a, tl, pt, blk, 0);
+  tile_positions(a, tl, pt, static_cast<int64_t>(blk) + nblk, 1);
+  pair_table(a, pt);
+  __syncthreads();
+  angle_table<D, IL>(a, pt, cs[0], tl.tok, 0);
+  __syncthreads();
+  int slot_i = 0, buf = 0;
+  for (int64_t item = blk; item < tl.items; item += nblk, buf ^= 1) {
+    const int64_t b = item / tl.per, n = (item - b * tl.per) * tl.tok + w.tok;
+    Angles ang;
+    load_angles<LPR>(cs[buf] + w.tok * D, c, u, ang);
+    Turn tn;
+    make_turn<IL>(ang, tn);
+    int left = n < a.N ? mine_h : 0;
+    T* out = static_cast<T*>(a.out[t]) + b * a.so[t][0] + n * a.so[t][2] + w.h0 * a.so[t][1] + u.off_a;
+    for (int j = iters; j > 0; --j, --left, out += so) {
+      float2 ga[4], gb[4], xa[4], xb[4];
+      copy_wait<S - 2>();
+      const uint4* slot = mine + slot_i * 4 * U;
+      read_unit<T>(slot, ga);
+      read_unit<T>(slot + U, gb);
+      read_unit<T>(slot + 2 * U, xa);
+      read_unit<T>(slot + 3 * U, xb);
+      slot_i = slot_i + 1 == S ? 0 : slot_i + 1;
+      issue();                            // into the slot that the last step read
+      turn<IL>(ga, gb, tn);
+      // sums of x^2 and of g w x
+      float2 ss = make_float2(0.f, 0.f), st = ss, sw = ss, sv = ss;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        ss = __ffma2_rn(xa[i], xa[i], ss);
+        st = __ffma2_rn(xb[i], xb[i], st);
+        sw = __ffma2_rn(__fmul2_rn(ga[i], wa[i]), xa[i], sw);
+        sv = __ffma2_rn(__fmul2_rn(gb[i], wb[i]), xb[i], sv);
+      }
+      const float rstd = rsqrtf(row_sum<LPR>(__fadd2_rn(ss, st)) * (1.f / D) + a.eps);
+      // xhat mean(g w xhat) = x rstd^2 (sum g w x) / D
+      const float m = row_sum<LPR>(__fadd2_rn(sw, sv)) * (1.f / D) * rstd * rstd * rstd;
+      const float2 r2 = make_float2(rstd, rstd), nm2 = make_float2(-m, -m);
+      if (left > 0) {                     // other lanes hold an old row: they add nothing
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          ga[i] = __fmul2_rn(ga[i], r2);
+          gb[i] = __fmul2_rn(gb[i], r2);
+          acc_a[i] = __ffma2_rn(ga[i], xa[i], acc_a[i]);
+          acc_b[i] = __ffma2_rn(gb[i], xb[i], acc_b[i]);
+          ga[i] = __ffma2_rn(ga[i], wa[i], __fmul2_rn(xa[i], nm2));
+          gb[i] = __ffma2_rn(gb[i], wb[i], __fmul2_rn(xb[i], nm2));
+        }
+        store_unit<T>(out, ga);
+        store_unit<T>(out + ab, gb);
+      }
+    }
+    if (item + nblk < tl.items) {
+      angle_table<D, IL>(a, pt, cs[buf ^ 1], tl.tok, buf ^ 1);
+      tile_positions(a, tl, pt, item + 2 * static_cast<int64_t>(nblk), buf);
+      __syncthreads();
+    }
+  }
+  copy_wait<0>();
   // lanes of a warp that hold the same columns, then the warps
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    __syncthreads();
+  for (int i = 0; i < 8; ++i) {
+    const float2 v2 = i < 4 ? acc_a[i & 3] : acc_b[i & 3];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      float v = acc[t][i];
+    for (int e = 0; e < 2; ++e) {
+      float v = e ? v2.y : v2.x;
 #pragma unroll
       for (int o = LPR; o < 32; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-      if (lane < LPR) red[warp][(i < 8 ? u.off_a : u.off_b) + (i & 7)] = v;
+      if (lane < LPR) red[warp][(i < 4 ? u.off_a : u.off_b) + 2 * (i & 3) + e] = v;
     }
-    __syncthreads();
-    for (int d = threadIdx.x; d < D; d += kThreads) {
-      float v = 0.f;
+  }
+  __syncthreads();
+  for (int d = threadIdx.x; d < D; d += kThreads) {
+    float v = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) v += red[w][d];
-      a.dw_part[(static_cast<int64_t>(blockIdx.x) * 2 + t) * D + d] = v;
-    }
+    for (int i = 0; i < kWarps; ++i) v += red[i][d];
+    a.dw_part[static_cast<int64_t>(blockIdx.x) * D + d] = v;
   }
 }
 
-// dq_weight | dk_weight: the blocks' partial rows added up, 32 columns per
-// block, eight warps taking every eighth row.
-__global__ void __launch_bounds__(kThreads) weight_grad_kernel(const float* part, int nparts, int D,
-                                                               float* dqw, float* dkw) {
-  __shared__ float red[kWarps][32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int col = blockIdx.x * 32 + lane;          // of 2 * D (a multiple of 32)
+// dq_weight | dk_weight: the blocks' partial rows added up, 16 columns of one
+// tensor per block, sixteen groups of threads taking every sixteenth row.
+__global__ void __launch_bounds__(kThreads) weight_grad_kernel(const float* part, int split, int nparts,
+                                                               int D, float* dqw, float* dkw) {
+  __shared__ float red[16][16];
+  const int grp = threadIdx.x >> 4, col = threadIdx.x & 15;
+  const int t = static_cast<int>(blockIdx.x) * 16 >= D ? 1 : 0;
+  const int d = static_cast<int>(blockIdx.x) * 16 - (t ? D : 0) + col;
+  const int p0 = t ? split : 0, p1 = t ? nparts : split;
   float v = 0.f;
-  for (int p = warp; p < nparts; p += kWarps) v += __ldg(part + static_cast<int64_t>(p) * 2 * D + col);
-  red[warp][lane] = v;
+#pragma unroll 4
+  for (int p = p0 + grp; p < p1; p += 16) v += __ldg(part + static_cast<int64_t>(p) * D + d);
+  red[grp][col] = v;
   __syncthreads();
-  if (warp == 0) {
+  if (grp == 0) {
     v = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) v += red[w][lane];
-    if (col < D) dqw[col] = v;
-    else dkw[col - D] = v;
+    for (int w = 0; w < 16; ++w) v += red[w][col];
+    (t ? dkw : dqw)[d] = v;
   }
 }
 
-// Tokens per tile: as many as keep the grid at four blocks per SM or more, so
-// that short inputs spread over the SMs.
-int pick_tile(int64_t B, int64_t N) {
-  int tile = kMaxTile;
-  while (tile > 1 && B * ((N + tile - 1) / tile) < 4 * static_cast<int64_t>(device_sm_count())) tile /= 2;
-  return tile;
+// What a tile of `tok` tokens costs a block, in row steps of its warps: the
+// steps of the heads, and the tile's own work (its angles, of which each thread
+// forms tok * pairs / 256, its barrier and addresses).
+double head_cost(int64_t heads, int64_t D, int tok) {
+  const int64_t rpw = 512 / D, tpw = rpw < tok ? rpw : tok, groups = tok / tpw;
+  const int64_t step = kWarps / groups * (rpw / tpw);      // heads per step of all warps of a group
+  return static_cast<double>((heads + step - 1) / step);
+}
+double tile_cost(const RotaryParams& p, int tok) { return 0.7 + 0.35 * tok * p.pairs / kThreads; }
+
+Tiles make_tiles(const RotaryParams& p, int tok) {
+  Tiles t{};
+  t.tok = tok;
+  t.per = (p.N + tok - 1) / tok;
+  t.items = p.B * t.per;
+  return t;
+}
+
+// The tokens per tile with which `slots` blocks end first, walking tiles whose
+// heads cost `heads(tok)`.  Long tiles cost less in all, short ones spread short
+// inputs over the SMs and leave less of the last round idle.
+template <typename Cost>
+Tiles pick_tiles(const RotaryParams& p, int64_t slots, Cost heads, double* time) {
+  Tiles best{};
+  *time = 0;
+  for (int tok = static_cast<int>(2048 / p.D); tok >= 1; tok /= 2) {
+    const Tiles t = make_tiles(p, tok);
+    const int64_t grid = t.items < slots ? t.items : slots;
+    const double ms = static_cast<double>((t.items + grid - 1) / grid) * (heads(tok) + tile_cost(p, tok));
+    if (*time == 0 || ms < *time) {
+      *time = ms;
+      best = t;
+    }
+  }
+  return best;
 }
 
 RotArgs make_args(const RotaryParams& p) {
@@ -399,14 +717,10 @@ RotArgs make_args(const RotaryParams& p) {
       a.sx[t][i] = p.sx[t][i]; a.sin[t][i] = p.sin[t][i]; a.so[t][i] = p.so[t][i];
     }
     a.heads[t] = static_cast<int>(t ? p.Hkv : p.Hq);
-    a.h_fast[t] = p.sx[t][1] <= p.sx[t][2];
     a.w[t] = p.w[t];
   }
   a.N = p.N;
-  a.tile = pick_tile(p.B, p.N);
-  a.tiles = static_cast<int>((p.N + a.tile - 1) / a.tile);
-  a.items = p.B * a.tiles;
-  a.pairs = p.pairs; a.interleaved = p.interleaved; a.naxes = p.naxes;
+  a.pairs = p.pairs; a.naxes = p.naxes;
   for (int i = 0; i < 4; ++i) a.sec_end[i] = p.sec_end[i];
   a.inv_freq = p.inv_freq; a.pos = p.pos; a.pos64 = p.pos64;
   for (int i = 0; i < 3; ++i) a.ps[i] = p.ps[i];
@@ -414,26 +728,66 @@ RotArgs make_args(const RotaryParams& p) {
   return a;
 }
 
+template <typename T, int D, bool NORM, bool IL>
+fa_status run_fwd(const RotaryParams& p, cudaStream_t s) {
+  const int64_t slots = static_cast<int64_t>(device_sm_count()) * fwd_blocks<T>(NORM);
+  RotArgs a = make_args(p);
+  double time;
+  a.tiles[0] = pick_tiles(p, slots, [&](int tok) { return head_cost(p.Hq, D, tok) + head_cost(p.Hkv, D, tok); },
+                          &time);
+  a.sign = p.backward ? -1.f : 1.f;      // without a norm the gradient is the rotation back
+  const int64_t grid = a.tiles[0].items < slots ? a.tiles[0].items : slots;
+  FA_CONFIGURE((rotary_kernel<T, D, NORM, IL>), kFwdSmem<T>);
+  rotary_kernel<T, D, NORM, IL><<<dim3(static_cast<unsigned>(grid)), dim3(kThreads), kFwdSmem<T>, s>>>(a);
+  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+}
+
+template <typename T, int D, bool IL>
+fa_status run_bwd(const RotaryParams& p, cudaStream_t s) {
+  const int64_t most = static_cast<int64_t>(device_sm_count()) * kBwdBlocks;
+  const int64_t slots = most < kRotaryMaxParts ? most : kRotaryMaxParts;
+  RotArgs a = make_args(p);
+  // The blocks dealt to q and k so that both end together: by their costs per
+  // token, and the shares around that one.
+  int64_t nq = 1, nk = 1;
+  double best = 0;
+  const int ref = static_cast<int>(1024 / D);
+  const double cq = head_cost(p.Hq, D, ref) + tile_cost(p, ref), ck = head_cost(p.Hkv, D, ref) + tile_cost(p, ref);
+  const int64_t mid = static_cast<int64_t>(static_cast<double>(slots) * cq / (cq + ck));
+  for (int64_t q = mid - 16; q <= mid + 16; q += 4) {
+    if (q < 1 || q >= slots) continue;
+    double tq, tk;
+    const Tiles lq = pick_tiles(p, q, [&](int tok) { return head_cost(p.Hq, D, tok); }, &tq);
+    const Tiles lk = pick_tiles(p, slots - q, [&](int tok) { return head_cost(p.Hkv, D, tok); }, &tk);
+    const double t = tq > tk ? tq : tk;
+    if (best == 0 || t < best) {
+      best = t;
+      a.tiles[0] = lq;
+      a.tiles[1] = lk;
+      nq = q < lq.items ? q : lq.items;
+      nk = slots - q < lk.items ? slots - q : lk.items;
+    }
+  }
+  a.sign = -1.f;
+  a.dw_part = p.ws;
+  a.split = static_cast<int>(nq);
+  FA_CONFIGURE((qk_norm_bwd_kernel<T, D, IL>), kBwdSmem<T>);
+  qk_norm_bwd_kernel<T, D, IL><<<dim3(static_cast<unsigned>(nq + nk)), dim3(kThreads), kBwdSmem<T>, s>>>(a);
+  if (cudaGetLastError() != cudaSuccess) return FA_ERR_LAUNCH;
+  weight_grad_kernel<<<dim3(2 * D / 16), dim3(kThreads), 0, s>>>(
+      p.ws, a.split, static_cast<int>(nq + nk), D, p.dw[0], p.dw[1]);
+  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+}
+
+template <typename T, int D, bool IL>
+fa_status run_layout(const RotaryParams& p, cudaStream_t s) {
+  if (p.w[0] == nullptr) return run_fwd<T, D, false, IL>(p, s);
+  return p.backward ? run_bwd<T, D, IL>(p, s) : run_fwd<T, D, true, IL>(p, s);
+}
+
 template <typename T, int D>
 fa_status run_rotary(const RotaryParams& p, cudaStream_t s) {
-  RotArgs a = make_args(p);
-  if (a.items > 0x7fffffffLL) return FA_ERR_SHAPE;
-  const bool norm = p.w[0] != nullptr;
-  if (p.backward && norm) {
-    a.sign = -1.f;
-    a.dw_part = p.ws;
-    const int64_t grid = a.items < kRotaryMaxParts ? a.items : kRotaryMaxParts;
-    qk_norm_bwd_kernel<T, D><<<dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s>>>(a);
-    if (cudaGetLastError() != cudaSuccess) return FA_ERR_LAUNCH;
-    weight_grad_kernel<<<dim3(2 * D / 32), dim3(kThreads), 0, s>>>(
-        p.ws, static_cast<int>(grid), D, p.dw[0], p.dw[1]);
-  } else {
-    a.sign = p.backward ? -1.f : 1.f;
-    const dim3 grid(static_cast<unsigned>(a.items));
-    if (norm) rotary_kernel<T, D, true><<<grid, dim3(kThreads), 0, s>>>(a);
-    else rotary_kernel<T, D, false><<<grid, dim3(kThreads), 0, s>>>(a);
-  }
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+  return p.interleaved ? run_layout<T, D, true>(p, s) : run_layout<T, D, false>(p, s);
 }
 
 template <typename T>

@@ -394,9 +394,9 @@ FA_API fa_status fa_bwd_prefix(const fa_problem* prob, int64_t P, const void* q,
  *              positions along that dimension
  *   q_weight, k_weight, weight_f32, eps
  *              both NULL: rotation only.  Both set: DEVICE arrays of D weights
- *              (fp32 when weight_f32, else of type dtype); each head x is first
- *              replaced by  x * rstd * weight,  rstd = (sum x^2 / D + eps)^(-1/2),
- *              eps finite and >= 0.
+ *              (fp32 when weight_f32, else of type dtype; 16-byte aligned);
+ *              each head x is first replaced by  x * rstd * weight,
+ *              rstd = (sum x^2 / D + eps)^(-1/2),  eps finite and >= 0.
  *
  * fa_rotary_fwd writes qo and ko:  a' = a cos - b sin,  b' = a sin + b cos  for
  * each pair (a, b).  All arithmetic is fp32, rounded to dtype once at the end.

@@ -70,7 +70,7 @@ def test_rotary_gradient_validation(lib):
     assert lib.fa_rotary_bwd_workspace_bytes(ctypes.byref(_rot())) == 0
     assert lib.fa_rotary_bwd_workspace_bytes(None) == 0
     need = lib.fa_rotary_bwd_workspace_bytes(ctypes.byref(_rot(**norm)))
-    assert need > 0 and need % (2 * 64 * 4) == 0
+    assert need > 0 and need % (64 * 4) == 0
 
     def bwd(pr, q=FAKE, dwq=FAKE, ws=FAKE, nbytes=need, dk=FAKE):
         return lib.fa_rotary_bwd(ctypes.byref(pr), q, ST, FAKE, ST, FAKE, ST, FAKE, ST, FAKE, ST, dk, ST,
