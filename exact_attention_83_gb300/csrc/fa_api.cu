@@ -225,6 +225,7 @@ fa_status run_fwd(const Problem& pb, const void* q, const int64_t* sq, const voi
     p.withhold_arrival = g_withhold_next.exchange(0);
     return launch_fwd_tc(p, stream);   // stores the keep mask as it draws it
   }
+  if (p.pfx.on) return launch_fwd_prefix_ffma(p, stream);
   FA_TRY(launch_fwd_ffma(p, stream));
   // the FFMA forward draws inline and stores nothing: fill the caller's keep
   // mask for the backward
@@ -551,7 +552,7 @@ fa_status fa_bwd_prefix(const fa_problem* prob, int64_t P, const void* q, const 
   for (int i = 0; i < 4; ++i) { p.sdkp[i] = sdkp4[i]; p.sdvp[i] = sdvp4[i]; }
   p.prof = nullptr;
   if (use_tc(pb.dtype) && have_bwd_tc(pb.D, pb.dtype)) return launch_bwd_tc(p, stream);
-  return launch_bwd_ffma(p, stream);
+  return launch_bwd_prefix_ffma(p, stream);
 }
 
 size_t fa_dropout_mask_bytes(const fa_problem* prob) {

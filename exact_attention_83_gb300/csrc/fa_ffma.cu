@@ -62,7 +62,6 @@ struct FfmaArgs {
   int causal;
   float scale;
   Dropout drop;
-  Prefix pfx;            // keys in front of every sequence's own (template flag PFX)
   unsigned int* status;
   const BwdParams* bp;   // host-side only: the call's parameters (profiling events)
 };
@@ -86,7 +85,7 @@ __device__ __forceinline__ float drop_factor(const Dropout& d, int64_t i, int64_
   return ((bits >> (j & 7)) & 1u) ? d.rscale : 0.f;
 }
 
-template <typename T, int D, bool PFX>
+template <typename T, int D>
 __global__ void __launch_bounds__(NT) fwd_ffma_kernel(FfmaArgs a) {
   extern __shared__ float sm[];
   constexpr int LD = D + 1, E = D / 16;
@@ -103,10 +102,12 @@ __global__ void __launch_bounds__(NT) fwd_ffma_kernel(FfmaArgs a) {
     if (threadIdx.x == 0) record_status(a.status, FA_ERR_SEQLENS);
     return;
   }
-  const int64_t Nq = sv.nq;
+  const int64_t Nq = sv.nq, Nk = sv.nk;
   const int64_t q0 = qt * BT;
   if (q0 >= Nq) return;
   const T* q = static_cast<const T*>(a.q) + sv.b * a.sq[0] + h * a.sq[1] + sv.q0 * a.sq[2];
+  const T* k = static_cast<const T*>(a.k) + sv.b * a.sk[0] + hk * a.sk[1] + sv.k0 * a.sk[2];
+  const T* v = static_cast<const T*>(a.v) + sv.b * a.sv[0] + hk * a.sv[1] + sv.k0 * a.sv[2];
   T* o = static_cast<T*>(a.o) + sv.b * a.so[0] + h * a.so[1] + sv.q0 * a.so[2];
   stage_tile<T, D>(Qs, q, a.sq[2], q0, Nq);
 
@@ -118,20 +119,11 @@ __global__ void __launch_bounds__(NT) fwd_ffma_kernel(FfmaArgs a) {
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[i][e] = 0.f;
   }
-  // with a prefix: its keys, all seen, then the sequence's own
-  for (int seg = PFX ? 0 : 1; seg < 2; ++seg) {
-  const bool pre = PFX && seg == 0, causal = a.causal && !pre;
-  const int64_t Nk = pre ? a.pfx.P : sv.nk;
-  const int64_t skn = pre ? a.pfx.sk[2] : a.sk[2], svn = pre ? a.pfx.sv[2] : a.sv[2];
-  const T* k = pre ? static_cast<const T*>(a.pfx.k) + hk * a.pfx.sk[1]
-                   : static_cast<const T*>(a.k) + sv.b * a.sk[0] + hk * a.sk[1] + sv.k0 * a.sk[2];
-  const T* v = pre ? static_cast<const T*>(a.pfx.v) + hk * a.pfx.sv[1]
-                   : static_cast<const T*>(a.v) + sv.b * a.sv[0] + hk * a.sv[1] + sv.k0 * a.sv[2];
-  const int64_t kend = causal ? min(Nk, q0 + BT) : Nk;
+  const int64_t kend = a.causal ? min(Nk, q0 + BT) : Nk;
   for (int64_t k0 = 0; k0 < kend; k0 += BT) {
     __syncthreads();
-    stage_tile<T, D>(Ks, k, skn, k0, Nk);
-    stage_tile<T, D>(Vs, v, svn, k0, Nk);
+    stage_tile<T, D>(Ks, k, a.sk[2], k0, Nk);
+    stage_tile<T, D>(Vs, v, a.sv[2], k0, Nk);
     __syncthreads();
     float s[4][4];
 #pragma unroll
@@ -152,14 +144,14 @@ __global__ void __launch_bounds__(NT) fwd_ffma_kernel(FfmaArgs a) {
     }
     // Ragged keys past N and (on the diagonal tile) keys after the query are
     // excluded.  Interior tiles skip the test.
-    const bool edge = (k0 + BT > Nk) || (causal && k0 + BT - 1 > q0);
+    const bool edge = (k0 + BT > Nk) || (a.causal && k0 + BT - 1 > q0);
     if (edge) {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int64_t kp = k0 + tx + 16 * j, qp = q0 + ty * 4 + i;
-          if (kp >= Nk || (causal && kp > qp)) s[i][j] = -INFINITY;
+          if (kp >= Nk || (a.causal && kp > qp)) s[i][j] = -INFINITY;
         }
     }
 #pragma unroll
@@ -198,7 +190,6 @@ __global__ void __launch_bounds__(NT) fwd_ffma_kernel(FfmaArgs a) {
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[i][e] = fmaf(p[i], vv[e], acc[i][e]);
     }
-  }
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -333,7 +324,7 @@ __global__ void __launch_bounds__(NT) bwd_dkdv_ffma_kernel(FfmaArgs a) {
 }
 
 // dQ: one CTA per (head, query tile); loops over the key tiles it attends to.
-template <typename T, int D, bool PFX>
+template <typename T, int D>
 __global__ void __launch_bounds__(NT) bwd_dq_ffma_kernel(FfmaArgs a) {
   extern __shared__ float sm[];
   constexpr int LD = D + 1, E = D / 16;
@@ -351,10 +342,12 @@ __global__ void __launch_bounds__(NT) bwd_dq_ffma_kernel(FfmaArgs a) {
     if (threadIdx.x == 0) record_status(a.status, FA_ERR_SEQLENS);
     return;
   }
-  const int64_t Nq = sv.nq;
+  const int64_t Nq = sv.nq, Nk = sv.nk;
   const int64_t q0 = qt * BT;
   if (q0 >= Nq) return;
   const T* q = static_cast<const T*>(a.q) + sv.b * a.sq[0] + h * a.sq[1] + sv.q0 * a.sq[2];
+  const T* k = static_cast<const T*>(a.k) + sv.b * a.sk[0] + hk * a.sk[1] + sv.k0 * a.sk[2];
+  const T* v = static_cast<const T*>(a.v) + sv.b * a.sv[0] + hk * a.sv[1] + sv.k0 * a.sv[2];
   const T* g = static_cast<const T*>(a.dout) + sv.b * a.sdo[0] + h * a.sdo[1] + sv.q0 * a.sdo[2];
   stage_tile<T, D>(Qs, q, a.sq[2], q0, Nq);
   stage_tile<T, D>(dOs, g, a.sdo[2], q0, Nq);
@@ -369,20 +362,11 @@ __global__ void __launch_bounds__(NT) bwd_dq_ffma_kernel(FfmaArgs a) {
 #pragma unroll
     for (int e = 0; e < E; ++e) dq[i][e] = 0.f;
   }
-  // with a prefix: its keys, all seen, then the sequence's own
-  for (int seg = PFX ? 0 : 1; seg < 2; ++seg) {
-  const bool pre = PFX && seg == 0, causal = a.causal && !pre;
-  const int64_t Nk = pre ? a.pfx.P : sv.nk;
-  const int64_t skn = pre ? a.pfx.sk[2] : a.sk[2], svn = pre ? a.pfx.sv[2] : a.sv[2];
-  const T* k = pre ? static_cast<const T*>(a.pfx.k) + hk * a.pfx.sk[1]
-                   : static_cast<const T*>(a.k) + sv.b * a.sk[0] + hk * a.sk[1] + sv.k0 * a.sk[2];
-  const T* v = pre ? static_cast<const T*>(a.pfx.v) + hk * a.pfx.sv[1]
-                   : static_cast<const T*>(a.v) + sv.b * a.sv[0] + hk * a.sv[1] + sv.k0 * a.sv[2];
-  const int64_t kend = causal ? min(Nk, q0 + BT) : Nk;
+  const int64_t kend = a.causal ? min(Nk, q0 + BT) : Nk;
   for (int64_t k0 = 0; k0 < kend; k0 += BT) {
     __syncthreads();
-    stage_tile<T, D>(Ks, k, skn, k0, Nk);
-    stage_tile<T, D>(Vs, v, svn, k0, Nk);
+    stage_tile<T, D>(Ks, k, a.sk[2], k0, Nk);
+    stage_tile<T, D>(Vs, v, a.sv[2], k0, Nk);
     __syncthreads();
     float s[4][4], dp[4][4];
 #pragma unroll
@@ -409,7 +393,7 @@ __global__ void __launch_bounds__(NT) bwd_dq_ffma_kernel(FfmaArgs a) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int64_t kp = k0 + tx + 16 * j, qp = q0 + ty * 4 + i;
-        const bool keep = kp < Nk && (!causal || kp <= qp);
+        const bool keep = kp < Nk && (!a.causal || kp <= qp);
         const float p = keep ? exp2f(fmaf(s[i][j], c, -L2[i])) : 0.f;
         const float z = a.drop.on ? drop_factor(a.drop, qp, kp, bh) : 1.f;
         dSs[(ty * 4 + i) * PLD + tx + 16 * j] = p * fmaf(z, dp[i][j], -Dl[i]);
@@ -427,7 +411,6 @@ __global__ void __launch_bounds__(NT) bwd_dq_ffma_kernel(FfmaArgs a) {
 #pragma unroll
         for (int e = 0; e < E; ++e) dq[i][e] = fmaf(ds[i], kv[e], dq[i][e]);
     }
-  }
   }
   T* dqp = static_cast<T*>(a.dq) + sv.b * a.sdq[0] + h * a.sdq[1] + sv.q0 * a.sdq[2];
 #pragma unroll
@@ -455,8 +438,7 @@ fa_status launch(Kern kern, size_t smem, int64_t blocks, const FfmaArgs& a, cuda
 
 template <typename T, int D>
 fa_status run_fwd(const FfmaArgs& a, cudaStream_t s) {
-  if (a.pfx.on) return launch(fwd_ffma_kernel<T, D, true>, fwd_smem(D), a.BH * a.ntiles, a, s);
-  return launch(fwd_ffma_kernel<T, D, false>, fwd_smem(D), a.BH * a.ntiles, a, s);
+  return launch(fwd_ffma_kernel<T, D>, fwd_smem(D), a.BH * a.ntiles, a, s);
 }
 template <typename T, int D>
 fa_status run_bwd(const FfmaArgs& a0, cudaStream_t s) {
@@ -465,24 +447,9 @@ fa_status run_bwd(const FfmaArgs& a0, cudaStream_t s) {
   a.BH = a.g.B * a.g.Hkv; a.ntiles = (a.g.Nk + BT - 1) / BT;
   fa_status st = launch(bwd_dkdv_ffma_kernel<T, D>, dkdv_smem(D), a.BH * a.ntiles, a, s);
   if (st != FA_OK) return st;
-  if (a.pfx.on && a.pfx.P > 0) {
-    // dK / dV of the prefix: every packed query row against it, as one sequence
-    const BwdParams& p = *a.bp;
-    FfmaArgs b = a;
-    b.g = prefix_geo(a.g, a.pfx.P);
-    b.k = a.pfx.k; b.v = a.pfx.v; b.dk = p.dkp; b.dv = p.dvp;
-    for (int i = 0; i < 4; ++i) {
-      b.sk[i] = a.pfx.sk[i]; b.sv[i] = a.pfx.sv[i]; b.sdk[i] = p.sdkp[i]; b.sdv[i] = p.sdvp[i];
-    }
-    b.causal = 0;
-    b.BH = b.g.Hkv; b.ntiles = (b.g.Nk + BT - 1) / BT;
-    st = launch(bwd_dkdv_ffma_kernel<T, D>, dkdv_smem(D), b.BH * b.ntiles, b, s);
-    if (st != FA_OK) return st;
-  }
   prof_record(*a.bp, 1, s);
   a.BH = a.g.B * a.g.Hq; a.ntiles = (a.g.Nq + BT - 1) / BT;
-  st = a.pfx.on ? launch(bwd_dq_ffma_kernel<T, D, true>, dq_smem(D), a.BH * a.ntiles, a, s)
-                : launch(bwd_dq_ffma_kernel<T, D, false>, dq_smem(D), a.BH * a.ntiles, a, s);
+  st = launch(bwd_dq_ffma_kernel<T, D>, dq_smem(D), a.BH * a.ntiles, a, s);
   prof_record(*a.bp, 2, s);
   return st;
 }
@@ -516,7 +483,6 @@ fa_status launch_fwd_ffma(const FwdParams& p, cudaStream_t s) {
   a.g = p.g; a.BH = p.g.B * p.g.Hq; a.ntiles = (p.g.Nq + BT - 1) / BT;
   copy4(a.sq, p.sq); copy4(a.sk, p.sk); copy4(a.sv, p.sv); copy4(a.so, p.so);
   a.causal = p.causal; a.scale = p.scale; a.drop = p.drop; a.status = p.status;
-  a.pfx = p.pfx;
   FA_DISPATCH(run_fwd, p.dtype, p.D, a, s);
 }
 
@@ -529,7 +495,6 @@ fa_status launch_bwd_ffma(const BwdParams& p, cudaStream_t s) {
   copy4(a.sdq, p.sdq); copy4(a.sdk, p.sdk); copy4(a.sdv, p.sdv);
   a.causal = p.causal; a.scale = p.scale; a.drop = p.drop; a.status = p.status;
   a.bp = &p;
-  a.pfx = p.pfx;
   FA_DISPATCH(run_bwd, p.dtype, p.D, a, s);
 }
 

@@ -279,6 +279,8 @@ inline void prof_record(const BwdParams& p, int i, cudaStream_t s) {
 // FA_ERR_ARG when it has no kernel compiled for the (D, dtype) asked for.
 fa_status launch_fwd_ffma(const FwdParams& p, cudaStream_t s);
 fa_status launch_bwd_ffma(const BwdParams& p, cudaStream_t s);
+fa_status launch_fwd_prefix_ffma(const FwdParams& p, cudaStream_t s);   // pfx.on
+fa_status launch_bwd_prefix_ffma(const BwdParams& p, cudaStream_t s);
 fa_status launch_preprocess(const PreParams& p, cudaStream_t s);
 fa_status launch_fwd_tc(const FwdParams& p, cudaStream_t s);
 fa_status launch_bwd_tc(const BwdParams& p, cudaStream_t s);
