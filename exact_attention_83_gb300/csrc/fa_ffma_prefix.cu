@@ -6,20 +6,26 @@
 // P rebuilt from L in the gradient) with two sets of keys per query: the
 // prefix's, all seen, then the sequence's own.  These problems are often small
 // (a few short sequences), so the shape differs from that file's:
-//  * a block owns 16 TM rows (TM = 2, or 1 when that leaves SMs without a block)
-//    and walks tiles of 64 rows of the other side, which are copied a tile ahead
-//    (cp.async for fp32);
-//  * operands are read from shared memory four at a time along the contraction
-//    (rows padded to D + 4 floats: the 16 rows that a half-warp reads start 16
-//    bytes apart in the banks); every product is still one fp32 FMA per term, in
-//    the order of the contraction;
+//  * a block has TM TY rows and 16 TY threads, each with TM x 4 of the scores,
+//    and walks tiles of 64 rows of the other side, copied a tile ahead (cp.async
+//    for fp32).  Operands are read from shared memory four at a time along the
+//    contraction (rows padded to D + 4 floats: the eight rows that a quarter of a
+//    warp reads cover all banks).  Small problems take 16 rows in four warps
+//    (TM = 2, one warp per scheduler; two warps of TM = 4 issued half as fast);
+//    where blocks of 64 rows (32 for the gradient at D = 128; TM = 4) come to two
+//    per SM, those read the walked tiles a quarter as often;
+//  * where even those leave SMs idle, a cluster of up to four blocks deals the
+//    tiles of one walk out and joins its sums through distributed shared memory
+//    (in the order of the blocks);
+//  * every product is one fp32 FMA per term, in the order of the contraction;
 //  * the gradient is one launch: blocks for dK / dV of the prefix (every packed
-//    query row against it, the longest loops, first), for dK / dV of the own
+//    query row against it, the longest walks, first), for dK / dV of the own
 //    keys and for dQ.  They share only inputs, and three launches in turn each
-//    left most of the GPU idle.  3 sequences of up to 130 rows, 4 heads of 64,
-//    200 prefix keys: forward 65 -> see kernel table, gradient 282 us before.
-// What bounds them is the shared-memory reads beside the FMAs at TM = 2 and the
-// latency of one block's steps when the grid is small.
+//    left most of the GPU idle.
+// 3 sequences of up to 130 rows, 4 heads of 64, 200 prefix keys: forward 18 us,
+// gradient 33 us (three launches of 64-row blocks with one operand per read:
+// 65 and 282).  Bound by the instructions of one block's steps, four warps per
+// SM; at large sizes by shared-memory reads, twice the FMAs' time.
 
 #include "tc_common.cuh"
 
@@ -29,7 +35,6 @@ namespace fa {
 namespace {
 
 constexpr int BC = 64;        // rows of a walked tile
-constexpr int NT = 256;       // threads: 16 x 16
 constexpr int PLD = BC + 4;   // leading dimension of P and dS
 
 struct Args {
@@ -42,12 +47,13 @@ struct Args {
   int causal;
   float scale;
   int64_t n_pre, n_own;       // gradient: blocks of the prefix's and the own keys' dK / dV
+  int cl;                     // blocks (one cluster) that share a walk
   unsigned int* status;
 };
 
 // Copies rows [row0, row0 + ROWS) of a strided N x D matrix into fp32 rows of
 // D + 4; rows at or past N are zero.  fp32 rows arrive asynchronously.
-template <typename T, int D, int ROWS>
+template <typename T, int D, int ROWS, int NT>
 __device__ __forceinline__ void stage(float* dst, const T* base, int64_t sn, int64_t row0, int64_t N) {
   constexpr int VEC = 16 / sizeof(T), UN = D / VEC, LD = D + 4;
   for (int idx = threadIdx.x; idx < ROWS * UN; idx += NT) {
@@ -102,6 +108,43 @@ __device__ __forceinline__ void store_cols(T* row, int tx, const float (&x)[D / 
 #pragma unroll
   for (int e = 0; e < C::E; ++e)
     row[(e / C::VW) * 16 * C::VW + C::VW * tx + e % C::VW] = Elem<T>::from_f32(x[e] * mul);
+}
+
+template <int D>
+__device__ __forceinline__ void put_cols(float* row, int tx, const float (&x)[D / 16]) {
+  using C = Cols<D>;
+#pragma unroll
+  for (int e = 0; e < C::E; ++e) row[(e / C::VW) * 16 * C::VW + C::VW * tx + e % C::VW] = x[e];
+}
+
+// Sums of a cluster's blocks: `part` (ROWS rows of D floats in every block's
+// shared memory, published by a cluster barrier), times w(rank, row), in the
+// order of the ranks; four elements at a time to put(row, column, sum).  Block
+// `rank` takes every cl-th row.
+template <int D, int ROWS, int NT, typename W, typename Put>
+__device__ __forceinline__ void join_cluster(const float* part, int rank, int cl, W w, Put put) {
+  for (int idx = threadIdx.x; idx < ROWS / cl * (D / 4); idx += NT) {
+    const int row = (idx / (D / 4)) * cl + rank, col = 4 * (idx % (D / 4));
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int r = 0; r < cl; ++r) {
+      const float4 x = tc::ld_cluster_f4(tc::cluster_map(tc::smem_u32(part + row * D + col), static_cast<uint32_t>(r)));
+      const float f = w(r, row);
+      sum.x = fmaf(f, x.x, sum.x); sum.y = fmaf(f, x.y, sum.y);
+      sum.z = fmaf(f, x.z, sum.z); sum.w = fmaf(f, x.w, sum.w);
+    }
+    put(row, col, sum);
+  }
+}
+template <typename T>
+__device__ __forceinline__ void store4(T* p, const float4& x, float mul) {
+  p[0] = Elem<T>::from_f32(x.x * mul); p[1] = Elem<T>::from_f32(x.y * mul);
+  p[2] = Elem<T>::from_f32(x.z * mul); p[3] = Elem<T>::from_f32(x.w * mul);
+}
+__device__ __forceinline__ float ld_cluster(const float* p, int rank) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];"
+               : "=f"(v) : "r"(tc::cluster_map(tc::smem_u32(p), static_cast<uint32_t>(rank))) : "memory");
+  return v;
 }
 
 __device__ __forceinline__ float at(const float4& v, int i) {
@@ -173,11 +216,11 @@ __device__ __forceinline__ KeyWalk<T> key_walk(const Args& a, const SeqView& s, 
   w.n = w.np + static_cast<int>((kend + BC - 1) / BC);
   return w;
 }
-template <typename T, int D>
+template <typename T, int D, int NT>
 __device__ __forceinline__ void stage_keys(const KeyWalk<T>& w, int t, float* ks, float* vs) {
   const bool pre = t < w.np;
-  stage<T, D, BC>(ks, pre ? w.kp : w.k, pre ? w.skp : w.sk, w.first(t), w.keys(t));
-  stage<T, D, BC>(vs, pre ? w.vp : w.v, pre ? w.svp : w.sv, w.first(t), w.keys(t));
+  stage<T, D, BC, NT>(ks, pre ? w.kp : w.k, pre ? w.skp : w.sk, w.first(t), w.keys(t));
+  stage<T, D, BC, NT>(vs, pre ? w.vp : w.v, pre ? w.svp : w.sv, w.first(t), w.keys(t));
   }
 
 // Block id -> (flat head of the query side, query tile), longest tiles first
@@ -196,9 +239,9 @@ __device__ __forceinline__ bool query_block(const Args& a, int64_t id, int rows,
   return q0 < s.nq;
 }
 
-template <typename T, int D, int TM>
-__global__ void __launch_bounds__(NT) fwd_prefix_ffma_kernel(const __grid_constant__ Args a) {
-  constexpr int LD = D + 4, BR = 16 * TM;
+template <typename T, int D, int TY, int TM>
+__global__ void __launch_bounds__(16 * TY) fwd_prefix_ffma_kernel(const __grid_constant__ Args a) {
+  constexpr int LD = D + 4, NT = 16 * TY, BR = TM * TY;
   extern __shared__ __align__(16) float sm[];
   float* Qs = sm;
   float* KV = Qs + BR * LD;            // [2][K | V]
@@ -206,12 +249,13 @@ __global__ void __launch_bounds__(NT) fwd_prefix_ffma_kernel(const __grid_consta
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   SeqView s;
   int64_t h, q0;
-  if (!query_block(a, blockIdx.x, BR, s, h, q0)) return;
+  const int cl = a.cl, rank = static_cast<int>(blockIdx.x % cl);
+  if (!query_block(a, blockIdx.x / cl, BR, s, h, q0)) return;   // all blocks of a cluster alike
   const int64_t hk = h / a.g.G;
   const KeyWalk<T> w = key_walk<T>(a, s, hk, a.causal ? min(s.nk, q0 + BR) : s.nk);
-  stage<T, D, BR>(Qs, static_cast<const T*>(a.q) + s.b * a.sq[0] + h * a.sq[1] + s.q0 * a.sq[2], a.sq[2], q0,
+  stage<T, D, BR, NT>(Qs, static_cast<const T*>(a.q) + s.b * a.sq[0] + h * a.sq[1] + s.q0 * a.sq[2], a.sq[2], q0,
                   s.nq);
-  if (w.n > 0) stage_keys<T, D>(w, 0, KV, KV + BC * LD);
+  if (rank < w.n) stage_keys<T, D, NT>(w, rank, KV, KV + BC * LD);
   const float c = a.scale * kLog2e;
   float m[TM], l[TM], acc[TM][D / 16];
 #pragma unroll
@@ -220,13 +264,14 @@ __global__ void __launch_bounds__(NT) fwd_prefix_ffma_kernel(const __grid_consta
 #pragma unroll
     for (int e = 0; e < D / 16; ++e) acc[i][e] = 0.f;
   }
-  for (int t = 0; t < w.n; ++t) {
-    const float* Ks = KV + (t & 1) * 2 * BC * LD;
+  int buf = 0;
+  for (int t = rank; t < w.n; t += cl, buf ^= 1) {
+    const float* Ks = KV + buf * 2 * BC * LD;
     const float* Vs = Ks + BC * LD;
     stage_wait();
-    __syncthreads();                   // tile t is here, tile t - 1 is no longer read
-    if (t + 1 < w.n)
-      stage_keys<T, D>(w, t + 1, KV + ((t + 1) & 1) * 2 * BC * LD, KV + (((t + 1) & 1) * 2 + 1) * BC * LD);
+    __syncthreads();                   // this tile is here, the last one is no longer read
+    if (t + cl < w.n)
+      stage_keys<T, D, NT>(w, t + cl, KV + (buf ^ 1) * 2 * BC * LD, KV + ((buf ^ 1) * 2 + 1) * BC * LD);
     float sc[TM][4] = {};
     dots<D, TM>(Qs, Ks, ty, tx, sc);
     const int64_t k0 = w.first(t), nk = w.keys(t);
@@ -265,6 +310,43 @@ __global__ void __launch_bounds__(NT) fwd_prefix_ffma_kernel(const __grid_consta
     __syncwarp();
   }
   stage_wait();
+  if (cl > 1) {
+    __syncthreads();
+    float* part = KV;                  // [BR][D] sums, then [BR] maxima and [BR] sums of weights
+    float* ml = KV + BR * D;
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      put_cols<D>(part + (ty * TM + i) * D, tx, acc[i]);
+      if (tx == 0) {
+        ml[ty * TM + i] = m[i];
+        ml[BR + ty * TM + i] = l[i];
+      }
+    }
+    tc::cluster_sync_all();
+    // weights of the blocks' sums of a row, over the sum of all weights
+    if (threadIdx.x < BR) {
+      const int row = threadIdx.x;
+      float mx = -INFINITY, sum = 0.f;
+      for (int r = 0; r < cl; ++r) mx = fmaxf(mx, ld_cluster(ml + row, r));
+      const float ms = mx == -INFINITY ? 0.f : mx;
+      for (int r = 0; r < cl; ++r) {
+        const float f = exp2f(ld_cluster(ml + row, r) - ms);
+        Ps[row * PLD + r] = f;
+        sum = fmaf(ld_cluster(ml + BR + row, r), f, sum);
+      }
+      Ps[row * PLD + cl] = sum > 0.f ? 1.f / sum : 0.f;     // no key at all: O = 0
+      if (rank == 0 && q0 + row < s.nq)
+        a.lse[lse_index(a.g, s, h, q0 + row)] = sum > 0.f ? (ms + log2f(sum)) * kLn2 : -INFINITY;
+    }
+    __syncthreads();
+    T* o = static_cast<T*>(a.o) + s.b * a.so[0] + h * a.so[1] + (s.q0 + q0) * a.so[2];
+    join_cluster<D, BR, NT>(part, rank, cl, [&](int r, int row) { return Ps[row * PLD + r]; },
+                            [&](int row, int col, const float4& x) {
+                              if (q0 + row < s.nq) store4<T>(o + row * a.so[2] + col, x, Ps[row * PLD + cl]);
+                            });
+    tc::cluster_sync_all();            // no block leaves while another reads its sums
+    return;
+  }
   T* o = static_cast<T*>(a.o) + s.b * a.so[0] + h * a.so[1] + s.q0 * a.so[2];
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
@@ -279,11 +361,11 @@ __global__ void __launch_bounds__(NT) fwd_prefix_ffma_kernel(const __grid_consta
   }
 }
 
-// dK / dV of 16 TM keys: `g` and the key tensors are the sequences' own or the
+// dK / dV of TM TY keys: `g` and the key tensors are the sequences' own or the
 // prefix's.
-template <typename T, int D, int TM>
-__device__ __forceinline__ void dkdv_block(const Args& a, const Geo& g, bool pre, int64_t id, float* sm) {
-  constexpr int LD = D + 4, BR = 16 * TM;
+template <typename T, int D, int TY, int TM>
+__device__ __forceinline__ void dkdv_block(const Args& a, const Geo& g, bool pre, int64_t id, int rank, float* sm) {
+  constexpr int LD = D + 4, NT = 16 * TY, BR = TM * TY;
   float* Ks = sm;
   float* Vs = Ks + BR * LD;
   float* QG = Vs + BR * LD;            // [2][Q | dO]
@@ -303,18 +385,19 @@ __device__ __forceinline__ void dkdv_block(const Args& a, const Geo& g, bool pre
   const bool causal = a.causal && !pre;
   const int64_t* sk = pre ? a.pfx.sk : a.sk;
   const int64_t* sv = pre ? a.pfx.sv : a.sv;
-  stage<T, D, BR>(Ks, static_cast<const T*>(pre ? a.pfx.k : a.k) + hk * sk[1] + s.k0 * sk[2], sk[2], k0, s.nk);
-  stage<T, D, BR>(Vs, static_cast<const T*>(pre ? a.pfx.v : a.v) + hk * sv[1] + s.k0 * sv[2], sv[2], k0, s.nk);
+  stage<T, D, BR, NT>(Ks, static_cast<const T*>(pre ? a.pfx.k : a.k) + hk * sk[1] + s.k0 * sk[2], sk[2], k0, s.nk);
+  stage<T, D, BR, NT>(Vs, static_cast<const T*>(pre ? a.pfx.v : a.v) + hk * sv[1] + s.k0 * sv[2], sv[2], k0, s.nk);
   // the query tiles of every query head that reads these keys
   const int64_t first = causal ? k0 / BC : 0, tiles = (s.nq + BC - 1) / BC;
   const int64_t per = tiles > first ? tiles - first : 0, steps = per * g.G;
   auto load = [&](int64_t it, int buf) {
     const int64_t h = hk * g.G + it / per, q0 = (first + it % per) * BC;
     float* Qs = QG + buf * 2 * BC * LD;
-    stage<T, D, BC>(Qs, static_cast<const T*>(a.q) + h * a.sq[1] + s.q0 * a.sq[2], a.sq[2], q0, s.nq);
-    stage<T, D, BC>(Qs + BC * LD, static_cast<const T*>(a.dout) + h * a.sdo[1] + s.q0 * a.sdo[2], a.sdo[2], q0,
+    stage<T, D, BC, NT>(Qs, static_cast<const T*>(a.q) + h * a.sq[1] + s.q0 * a.sq[2], a.sq[2], q0, s.nq);
+    stage<T, D, BC, NT>(Qs + BC * LD, static_cast<const T*>(a.dout) + h * a.sdo[1] + s.q0 * a.sdo[2], a.sdo[2], q0,
                     s.nq);
-        if (threadIdx.x < BC) {
+        static_assert(NT >= BC, "one L and Delta per thread");
+    if (threadIdx.x < BC) {
       const int64_t row = q0 + threadIdx.x, li = lse_index(g, s, h, row);
       LDl[buf * 2 * BC + threadIdx.x] = row < s.nq ? a.lse_in[li] * kLog2e : 0.f;
       LDl[(buf * 2 + 1) * BC + threadIdx.x] = row < s.nq ? a.delta[li] : 0.f;
@@ -322,15 +405,16 @@ __device__ __forceinline__ void dkdv_block(const Args& a, const Geo& g, bool pre
   };
   const float c = a.scale * kLog2e;
   float dk[TM][D / 16] = {}, dv[TM][D / 16] = {};
-  if (steps > 0) load(0, 0);
-  for (int64_t it = 0; it < steps; ++it) {
-    const int buf = static_cast<int>(it & 1);
+  const int cl = a.cl;
+  if (rank < steps) load(rank, 0);
+  int buf = 0;
+  for (int64_t it = rank; it < steps; it += cl, buf ^= 1) {
     const float* Qs = QG + buf * 2 * BC * LD;
     const float* Gs = Qs + BC * LD;
     const int64_t q0 = (first + it % per) * BC;
     stage_wait();
     __syncthreads();
-    if (it + 1 < steps) load(it + 1, buf ^ 1);
+    if (it + cl < steps) load(it + cl, buf ^ 1);
     // element (key ty TM + i, query tx + 16 j)
     float sc[TM][4] = {}, dp[TM][4] = {};
     dots<D, TM>(Ks, Qs, ty, tx, sc);
@@ -356,6 +440,25 @@ __device__ __forceinline__ void dkdv_block(const Args& a, const Geo& g, bool pre
   const int64_t* sdv = pre ? a.sdvp : a.sdv;
   T* dkp = static_cast<T*>(pre ? a.dkp : a.dk) + hk * sdk[1] + s.k0 * sdk[2];
   T* dvp = static_cast<T*>(pre ? a.dvp : a.dv) + hk * sdv[1] + s.k0 * sdv[2];
+  if (cl > 1) {
+    __syncthreads();
+    float* part = QG;                  // [BR][D] of dK, then of dV
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      put_cols<D>(part + (ty * TM + i) * D, tx, dk[i]);
+      put_cols<D>(part + (BR + ty * TM + i) * D, tx, dv[i]);
+    }
+    tc::cluster_sync_all();
+    join_cluster<D, 2 * BR, NT>(part, rank, cl, [](int, int) { return 1.f; },
+                                [&](int row, int col, const float4& x) {
+                                  const int64_t key = k0 + row % BR;
+                                  if (key >= s.nk) return;
+                                  if (row < BR) store4<T>(dkp + key * sdk[2] + col, x, a.scale);
+                                  else store4<T>(dvp + key * sdv[2] + col, x, 1.f);
+                                });
+    tc::cluster_sync_all();
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
     const int64_t row = k0 + ty * TM + i;
@@ -365,9 +468,9 @@ __device__ __forceinline__ void dkdv_block(const Args& a, const Geo& g, bool pre
   }
 }
 
-template <typename T, int D, int TM>
-__device__ __forceinline__ void dq_block(const Args& a, int64_t id, float* sm) {
-  constexpr int LD = D + 4, BR = 16 * TM;
+template <typename T, int D, int TY, int TM>
+__device__ __forceinline__ void dq_block(const Args& a, int64_t id, int rank, float* sm) {
+  constexpr int LD = D + 4, NT = 16 * TY, BR = TM * TY;
   float* Qs = sm;
   float* Gs = Qs + BR * LD;
   float* KV = Gs + BR * LD;            // [2][K | V]
@@ -378,9 +481,10 @@ __device__ __forceinline__ void dq_block(const Args& a, int64_t id, float* sm) {
   if (!query_block(a, id, BR, s, h, q0)) return;
   const int64_t hk = h / a.g.G;
   const KeyWalk<T> w = key_walk<T>(a, s, hk, a.causal ? min(s.nk, q0 + BR) : s.nk);
-  stage<T, D, BR>(Qs, static_cast<const T*>(a.q) + h * a.sq[1] + s.q0 * a.sq[2], a.sq[2], q0, s.nq);
-  stage<T, D, BR>(Gs, static_cast<const T*>(a.dout) + h * a.sdo[1] + s.q0 * a.sdo[2], a.sdo[2], q0, s.nq);
-  if (w.n > 0) stage_keys<T, D>(w, 0, KV, KV + BC * LD);
+  stage<T, D, BR, NT>(Qs, static_cast<const T*>(a.q) + h * a.sq[1] + s.q0 * a.sq[2], a.sq[2], q0, s.nq);
+  stage<T, D, BR, NT>(Gs, static_cast<const T*>(a.dout) + h * a.sdo[1] + s.q0 * a.sdo[2], a.sdo[2], q0, s.nq);
+  const int cl = a.cl;
+  if (rank < w.n) stage_keys<T, D, NT>(w, rank, KV, KV + BC * LD);
   const float c = a.scale * kLog2e;
   float L2[TM], Dl[TM], dq[TM][D / 16] = {};
 #pragma unroll
@@ -389,13 +493,14 @@ __device__ __forceinline__ void dq_block(const Args& a, int64_t id, float* sm) {
     L2[i] = row < s.nq ? a.lse_in[li] * kLog2e : 0.f;
     Dl[i] = row < s.nq ? a.delta[li] : 0.f;
   }
-  for (int t = 0; t < w.n; ++t) {
-    const float* Ks = KV + (t & 1) * 2 * BC * LD;
+  int buf = 0;
+  for (int t = rank; t < w.n; t += cl, buf ^= 1) {
+    const float* Ks = KV + buf * 2 * BC * LD;
     const float* Vs = Ks + BC * LD;
     stage_wait();
     __syncthreads();
-    if (t + 1 < w.n)
-      stage_keys<T, D>(w, t + 1, KV + ((t + 1) & 1) * 2 * BC * LD, KV + (((t + 1) & 1) * 2 + 1) * BC * LD);
+    if (t + cl < w.n)
+      stage_keys<T, D, NT>(w, t + cl, KV + (buf ^ 1) * 2 * BC * LD, KV + ((buf ^ 1) * 2 + 1) * BC * LD);
     float sc[TM][4] = {}, dp[TM][4] = {};
     dots<D, TM>(Qs, Ks, ty, tx, sc);
     dots<D, TM>(Gs, Vs, ty, tx, dp);
@@ -416,6 +521,19 @@ __device__ __forceinline__ void dq_block(const Args& a, int64_t id, float* sm) {
   }
   stage_wait();
   T* out = static_cast<T*>(a.dq) + h * a.sdq[1] + s.q0 * a.sdq[2];
+  if (cl > 1) {
+    __syncthreads();
+    float* part = KV;                  // [BR][D]
+#pragma unroll
+    for (int i = 0; i < TM; ++i) put_cols<D>(part + (ty * TM + i) * D, tx, dq[i]);
+    tc::cluster_sync_all();
+    join_cluster<D, BR, NT>(part, rank, cl, [](int, int) { return 1.f; },
+                            [&](int row, int col, const float4& x) {
+                              if (q0 + row < s.nq) store4<T>(out + (q0 + row) * a.sdq[2] + col, x, a.scale);
+                            });
+    tc::cluster_sync_all();
+    return;
+  }
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
     const int64_t row = q0 + ty * TM + i;
@@ -423,53 +541,96 @@ __device__ __forceinline__ void dq_block(const Args& a, int64_t id, float* sm) {
   }
 }
 
-template <typename T, int D, int TM>
-__global__ void __launch_bounds__(NT) bwd_prefix_ffma_kernel(const __grid_constant__ Args a) {
+template <typename T, int D, int TY, int TM>
+__global__ void __launch_bounds__(16 * TY) bwd_prefix_ffma_kernel(const __grid_constant__ Args a) {
   extern __shared__ __align__(16) float sm[];
-  const int64_t id = blockIdx.x;
-  if (id < a.n_pre) dkdv_block<T, D, TM>(a, a.gp, true, id, sm);
-  else if (id < a.n_pre + a.n_own) dkdv_block<T, D, TM>(a, a.g, false, id - a.n_pre, sm);
-  else dq_block<T, D, TM>(a, id - a.n_pre - a.n_own, sm);
+  const int64_t id = blockIdx.x / a.cl;
+  const int rank = static_cast<int>(blockIdx.x % a.cl);
+  if (id < a.n_pre) dkdv_block<T, D, TY, TM>(a, a.gp, true, id, rank, sm);
+  else if (id < a.n_pre + a.n_own) dkdv_block<T, D, TY, TM>(a, a.g, false, id - a.n_pre, rank, sm);
+  else dq_block<T, D, TY, TM>(a, id - a.n_pre - a.n_own, rank, sm);
 }
 
-constexpr int fwd_smem(int D, int TM) { return 4 * ((16 * TM + 4 * BC) * (D + 4) + 16 * TM * PLD); }
-constexpr int bwd_smem(int D, int TM) {
-  return 4 * ((32 * TM + 4 * BC) * (D + 4) + 32 * TM * PLD + 4 * BC);
+constexpr int fwd_smem(int D, int BR) { return 4 * ((BR + 4 * BC) * (D + 4) + BR * PLD); }
+constexpr int bwd_smem(int D, int BR) {
+  return 4 * ((2 * BR + 4 * BC) * (D + 4) + 2 * BR * PLD + 4 * BC);
 }
-static_assert(bwd_smem(128, 2) <= 232448 && fwd_smem(128, 2) <= 232448, "shared memory per block");
+// TY of the large blocks (TM = 4)
+constexpr int fwd_big(int) { return 16; }
+constexpr int bwd_big(int D) { return D == 128 ? 8 : 16; }
+static_assert(bwd_smem(128, 4 * bwd_big(128)) <= 232448 && bwd_smem(64, 4 * bwd_big(64)) <= 232448 &&
+                  fwd_smem(128, 4 * fwd_big(128)) <= 232448, "shared memory per block");
 
 int64_t tiles(int64_t n, int rows) { return (n + rows - 1) / rows; }
 
-template <typename T, int D, int TM>
-fa_status launch_fwd(const Args& a, cudaStream_t s) {
-  const int64_t blocks = a.g.B * a.g.Hq * tiles(a.g.Nq, 16 * TM);
-  if (blocks > 0x7fffffffLL) return FA_ERR_SHAPE;
-  FA_CONFIGURE((fwd_prefix_ffma_kernel<T, D, TM>), fwd_smem(D, TM));
-  fwd_prefix_ffma_kernel<T, D, TM><<<dim3(static_cast<unsigned>(blocks)), dim3(NT), fwd_smem(D, TM), s>>>(a);
+int64_t fwd_blocks(const Args& a, int BR) { return a.g.B * a.g.Hq * tiles(a.g.Nq, BR); }
+
+// Blocks that share a walk of `steps` tiles, with `per_sm` blocks per SM at
+// most.  3 sequences of up to 130 rows behind 200 keys: forward 20.9 us with four
+// blocks to a walk (two rounds of blocks), 17.8 with the two that stay resident;
+// gradient 32.7 us at four per SM, 54 at the two that stay resident (its walks
+// are longer and of unequal lengths).
+int pick_cluster(int64_t blocks, int64_t steps, int64_t per_sm) {
+  const int64_t slots = static_cast<int64_t>(device_sm_count()) * per_sm;
+  int cl = 1;
+  while (cl < 4 && 2 * cl <= steps && blocks * 2 * cl <= slots) cl *= 2;
+  return cl;
+}
+
+template <typename Kern>
+fa_status launch(Kern kern, int64_t blocks, int threads, int smem, const Args& a, cudaStream_t s) {
+  if (blocks * a.cl > 0x7fffffffLL) return FA_ERR_SHAPE;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(blocks * a.cl));
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  if (a.cl > 1) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(a.cl);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+  }
+  if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) return FA_ERR_LAUNCH;
   return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
-template <typename T, int D, int TM>
+template <typename T, int D, int TY, int TM>
+fa_status launch_fwd(Args a, cudaStream_t s) {
+  const int64_t blocks = fwd_blocks(a, TM * TY);
+  a.cl = pick_cluster(blocks, tiles(a.pfx.P, BC) + tiles(a.g.Nk, BC),
+                      233472 / (fwd_smem(D, TM * TY) + 1024));
+  FA_CONFIGURE((fwd_prefix_ffma_kernel<T, D, TY, TM>), fwd_smem(D, TM * TY));
+  return launch(fwd_prefix_ffma_kernel<T, D, TY, TM>, blocks, 16 * TY, fwd_smem(D, TM * TY), a, s);
+}
+
+int64_t bwd_blocks(Args& a, int BR) {
+  a.n_pre = a.pfx.P > 0 ? a.g.Hkv * tiles(a.pfx.P, BR) : 0;
+  a.n_own = a.g.B * a.g.Hkv * tiles(a.g.Nk, BR);
+  return a.n_pre + a.n_own + a.g.B * a.g.Hq * tiles(a.g.Nq, BR);
+}
+
+template <typename T, int D, int TY, int TM>
 fa_status launch_bwd(Args a, cudaStream_t s) {
-  a.n_pre = a.pfx.P > 0 ? a.g.Hkv * tiles(a.pfx.P, 16 * TM) : 0;
-  a.n_own = a.g.B * a.g.Hkv * tiles(a.g.Nk, 16 * TM);
-  const int64_t blocks = a.n_pre + a.n_own + a.g.B * a.g.Hq * tiles(a.g.Nq, 16 * TM);
-  if (blocks > 0x7fffffffLL) return FA_ERR_SHAPE;
-  FA_CONFIGURE((bwd_prefix_ffma_kernel<T, D, TM>), bwd_smem(D, TM));
-  bwd_prefix_ffma_kernel<T, D, TM><<<dim3(static_cast<unsigned>(blocks)), dim3(NT), bwd_smem(D, TM), s>>>(a);
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+  const int64_t blocks = bwd_blocks(a, TM * TY);
+  a.cl = pick_cluster(blocks, tiles(a.pfx.P, BC) + tiles(a.g.Nk, BC), 4);
+  FA_CONFIGURE((bwd_prefix_ffma_kernel<T, D, TY, TM>), bwd_smem(D, TM * TY));
+  return launch(bwd_prefix_ffma_kernel<T, D, TY, TM>, blocks, 16 * TY, bwd_smem(D, TM * TY), a, s);
 }
 
-// TM = 1 when blocks of 32 rows leave SMs without one.
+// Large blocks where they come to two per SM.
 template <typename T, int D>
 fa_status run(const Args& a, bool bwd, cudaStream_t s) {
-  const int64_t sms = device_sm_count();
-  if (!bwd) {
-    return a.g.B * a.g.Hq * tiles(a.g.Nq, 32) < sms ? launch_fwd<T, D, 1>(a, s) : launch_fwd<T, D, 2>(a, s);
-  }
-  const int64_t blocks = a.g.Hkv * tiles(a.pfx.P, 32) + a.g.B * a.g.Hkv * tiles(a.g.Nk, 32) +
-                         a.g.B * a.g.Hq * tiles(a.g.Nq, 32);
-  return blocks < sms ? launch_bwd<T, D, 1>(a, s) : launch_bwd<T, D, 2>(a, s);
+  const int64_t enough = 2 * static_cast<int64_t>(device_sm_count());
+  if (!bwd)
+    return fwd_blocks(a, 4 * fwd_big(D)) >= enough ? launch_fwd<T, D, fwd_big(D), 4>(a, s)
+                                                   : launch_fwd<T, D, 8, 2>(a, s);
+  Args t = a;
+  return bwd_blocks(t, 4 * bwd_big(D)) >= enough ? launch_bwd<T, D, bwd_big(D), 4>(a, s)
+                                                 : launch_bwd<T, D, 8, 2>(a, s);
 }
 
 template <typename T>

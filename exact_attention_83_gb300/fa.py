@@ -148,7 +148,7 @@ _lock = threading.Lock()
 _lib = None
 _i64 = ctypes.c_int64
 _vp = ctypes.c_void_p
-_s4 = ctypes.POINTER(ctypes.c_int64)
+_s4 = ctypes.c_void_p      # int64[4]: a ctypes array or packed bytes
 
 
 def load_library(path: str = LIB_PATH):
@@ -537,18 +537,19 @@ def _apply_bwd(q, k, dqo, dko, rot, out):
     lib = load_library()
     if norm:
         D = dqo.shape[-1]
-        dw = torch.empty((2, D), dtype=torch.float32, device=q.device)
+        dev = q.device
+        dqw = torch.empty(D, dtype=torch.float32, device=dev)
+        dkw = torch.empty(D, dtype=torch.float32, device=dev)
         nbytes = lib.fa_rotary_bwd_workspace_bytes(pr)
-        ws = torch.empty(nbytes // 4, dtype=torch.float32, device=q.device)
-        dw0 = dw.data_ptr()
-        extra = (dw0, dw0 + 4 * D, ws.data_ptr(), nbytes)
+        ws = torch.empty(nbytes // 4, dtype=torch.float32, device=dev)
+        extra = (dqw.data_ptr(), dkw.data_ptr(), ws.data_ptr(), nbytes)
     else:
         q, k = dqo, dko
         extra = (0, 0, 0, 0)
     _call(lib.fa_rotary_bwd, "fa_rotary_bwd", dqo.get_device(), pr, q.data_ptr(), _strides4(q),
           k.data_ptr(), _strides4(k), dqo.data_ptr(), _strides4(dqo), dko.data_ptr(), _strides4(dko),
           dq.data_ptr(), _strides4(dq), dk.data_ptr(), _strides4(dk), *extra)
-    return (dq, dk, dw[0], dw[1]) if norm else (dq, dk)
+    return (dq, dk, dqw, dkw) if norm else (dq, dk)
 
 
 def rotary_fwd(q, k, positions, inv_freq, sections=None, interleaved: bool = False, out=None):
@@ -663,34 +664,40 @@ def decode(q, k_prefix, v_prefix, k, v, seq_lens, o, lse, causal: bool = True, s
     """fa_decode.  workspace: a contiguous CUDA tensor of at least
     decode_workspace_bytes(q, k_prefix, k) bytes, 16-byte aligned (None when
     that is 0); calls that may overlap on the GPU need one each."""
+    sizes = _decode_sizes(q, k_prefix, k)
+    if o.shape != q.shape or o.dtype != q.dtype or o.device != q.device:
+        raise ValueError("o: the shape, dtype and device of q")
+    if lse.dtype != torch.float32 or lse.shape != q.shape[:3] or lse.device != q.device \
+            or not lse.is_contiguous():
+        raise ValueError("lse: contiguous float32 [B, Hq, Nq] on q's device")
+    if workspace is not None and (workspace.device != q.device or not workspace.is_contiguous()):
+        raise ValueError("workspace: a contiguous tensor on q's device")
+    _decode(sizes, q, k_prefix, v_prefix, k, v, seq_lens, o, lse, causal, scale, workspace)
+
+
+def _decode(sizes, q, k_prefix, v_prefix, k, v, seq_lens, o, lse, causal, scale, workspace):
+    """decode with its outputs and workspace known to fit."""
     dt = q.dtype
     if (dt != torch.bfloat16 and dt != torch.float16) or not q.is_cuda:
         raise TypeError("decode takes CUDA float16 or bfloat16 tensors")
-    sizes = _decode_sizes(q, k_prefix, k)
     dev = q.get_device()
-    for t in (k_prefix, v_prefix, k, v, o):
+    for t in (k_prefix, v_prefix, k, v):
         if t.dtype != dt or t.get_device() != dev:
             raise ValueError("all tensors must share dtype and device")
-    if o.shape != q.shape or v.shape != k.shape or v_prefix.shape != k_prefix.shape:
-        raise ValueError("o, v and v_prefix take the shapes of q, k and k_prefix")
-    if lse.dtype != torch.float32 or lse.shape != q.shape[:3] or lse.get_device() != dev \
-            or not lse.is_contiguous():
-        raise ValueError("lse: contiguous float32 [B, Hq, Nq] on q's device")
-    if seq_lens.dtype != torch.int32 or seq_lens.dim() != 1 or seq_lens.numel() != sizes[0] \
-            or seq_lens.get_device() != dev or not seq_lens.is_contiguous():
+    if v.shape != k.shape or v_prefix.shape != k_prefix.shape:
+        raise ValueError("v and v_prefix take the shapes of k and k_prefix")
+    if seq_lens.dtype != torch.int32 or seq_lens.shape != (sizes[0],) or seq_lens.get_device() != dev \
+            or not seq_lens.is_contiguous():
         raise ValueError("seq_lens: a contiguous int32 vector of B lengths on q's device")
     ws = nbytes = 0
     if workspace is not None:
-        if workspace.get_device() != dev or not workspace.is_contiguous():
-            raise ValueError("workspace: a contiguous tensor on q's device")
         ws, nbytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     pr = _PACK_DECODE(*sizes, seq_lens.data_ptr(), bool(causal), _scale(sizes[4], scale),
                       _DTYPE_CODE[dt])
-    sp, svp = k_prefix.stride(), v_prefix.stride()
     _call(load_library().fa_decode, "fa_decode", dev, pr, q.data_ptr(), _PACK4(*q.stride()),
-          k_prefix.data_ptr(), _PACK4(0, *sp), v_prefix.data_ptr(), _PACK4(0, *svp), k.data_ptr(),
-          _PACK4(*k.stride()), v.data_ptr(), _PACK4(*v.stride()), o.data_ptr(),
-          _PACK4(*o.stride()), lse.data_ptr(), ws, nbytes)
+          k_prefix.data_ptr(), _PACK4(0, *k_prefix.stride()), v_prefix.data_ptr(),
+          _PACK4(0, *v_prefix.stride()), k.data_ptr(), _PACK4(*k.stride()), v.data_ptr(),
+          _PACK4(*v.stride()), o.data_ptr(), _PACK4(*o.stride()), lse.data_ptr(), ws, nbytes)
 
 
 def attention_decode(q, k_prefix, v_prefix, k, v, seq_lens, causal: bool = True, scale=None,
@@ -702,13 +709,16 @@ def attention_decode(q, k_prefix, v_prefix, k, v, seq_lens, causal: bool = True,
     CUDA vector; the new tokens' rows among them, as the last Nq).  causal: token
     t sees own rows up to its own.  float16 and bfloat16; no gradient."""
     sizes = _decode_sizes(q, k_prefix, k)
+    dev = q.device
     o = torch.empty_like(q, memory_format=torch.contiguous_format)
-    lse = torch.empty(sizes[0], sizes[1], sizes[3], dtype=torch.float32, device=q.device)
+    lse = torch.empty((sizes[0], sizes[1], sizes[3]), dtype=torch.float32, device=dev)
     if workspace is None:
         nbytes = _decode_bytes(sizes)
         if nbytes:
-            workspace = torch.empty(nbytes // 4, dtype=torch.float32, device=q.device)
-    decode(q, k_prefix, v_prefix, k, v, seq_lens, o, lse, causal, scale, workspace=workspace)
+            workspace = torch.empty(nbytes // 4, dtype=torch.float32, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace: a contiguous tensor on q's device")
+    _decode(sizes, q, k_prefix, v_prefix, k, v, seq_lens, o, lse, causal, scale, workspace)
     return o, lse
 
 
@@ -982,24 +992,27 @@ def attention_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, max_seqlen_q: int,
 # Packed sequences behind one shared prefix
 
 
-def _prefix_problem(q, k, k_prefix, cu_q, cu_k, max_q, max_k, causal, scale) -> bytes:
-    """struct fa_problem of a prefix call, its tensors' common checks done."""
+def _prefix_problem(q, k, v, k_prefix, v_prefix, cu_q, cu_k, max_q, max_k, causal, scale) -> bytes:
+    """struct fa_problem of a prefix call, its inputs checked."""
     dt = q.dtype
     if dt not in _DTYPE_CODE or not q.is_cuda:
         raise TypeError("tensors must be CUDA float32, float16 or bfloat16")
-    if q.dim() != 3 or k.dim() != 3 or k_prefix.dim() != 3:
+    qs, ks, ps = q.shape, k.shape, k_prefix.shape
+    if len(qs) != 3 or len(ks) != 3 or len(ps) != 3:
         raise ValueError("expected q [total_q, Hq, D], k, v [total_k, Hkv, D], prefixes [P, Hkv, D]")
     dev = q.get_device()
-    total_q, Hq, D = q.shape
-    total_k, Hkv, Dk = k.shape
-    if Dk != D or k_prefix.shape[1] != Hkv or k_prefix.shape[2] != D:
-        raise ValueError("q, k and the prefix must share head dimension and key/value heads")
+    if v.shape != ks or v_prefix.shape != ps or ks[2] != qs[2] or ps[1:] != ks[1:]:
+        raise ValueError("q, k, v and the prefixes must share head dimension and key/value heads")
+    for t in (k, v, k_prefix, v_prefix):
+        if t.dtype != dt or t.get_device() != dev:
+            raise ValueError("all tensors must share dtype and device")
+    n = cu_q.numel()
     for cu in (cu_q, cu_k):
         if cu.dtype != torch.int32 or cu.get_device() != dev or cu.dim() != 1 \
-                or not cu.is_contiguous() or cu.numel() != cu_q.numel() or cu.numel() < 2:
+                or not cu.is_contiguous() or cu.numel() != n or n < 2:
             raise ValueError("cu_seqlens_q and cu_seqlens_k: contiguous int32 CUDA vectors of B+1")
-    return _PACK_PROBLEM(cu_q.numel() - 1, Hq, Hkv, int(max_q), int(max_k), D, cu_q.data_ptr(),
-                         cu_k.data_ptr(), total_q, total_k, bool(causal), _scale(D, scale),
+    return _PACK_PROBLEM(n - 1, qs[1], ks[1], int(max_q), int(max_k), qs[2], cu_q.data_ptr(),
+                         cu_k.data_ptr(), qs[0], ks[0], bool(causal), _scale(qs[2], scale),
                          _DTYPE_CODE[dt], 0.0, 0, 0, 0)
 
 
@@ -1012,7 +1025,7 @@ def _like(ref, *ts):
 def _lse_like(q, *ts):
     for t in ts:
         if t.dtype != torch.float32 or t.device != q.device or not t.is_contiguous() \
-                or tuple(t.shape) != (q.shape[1], q.shape[0]):
+                or t.shape != (q.shape[1], q.shape[0]):
             raise ValueError("lse, delta: contiguous float32 [Hq, total_q] on q's device")
 
 
@@ -1021,21 +1034,26 @@ def _addr(*ts):
     return [x for t in ts for x in (t.data_ptr(), _strides4(t))]
 
 
+def _fwd_prefix(pr, q, k, v, k_prefix, v_prefix, o, lse):
+    _call(load_library().fa_fwd_prefix, "fa_fwd_prefix", q.get_device(), pr, k_prefix.shape[0],
+          *_addr(q, k_prefix, v_prefix, k, v, o), lse.data_ptr())
+
+
+def _bwd_prefix(pr, q, k, v, k_prefix, v_prefix, do, lse, delta, dq, dk, dv, dk_prefix, dv_prefix):
+    _call(load_library().fa_bwd_prefix, "fa_bwd_prefix", q.get_device(), pr, k_prefix.shape[0],
+          *_addr(q, k_prefix, v_prefix, k, v, do), lse.data_ptr(), delta.data_ptr(),
+          *_addr(dq, dk_prefix, dv_prefix, dk, dv))
+
+
 def fwd_prefix(q, k, v, k_prefix, v_prefix, o, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
                max_seqlen_k, causal: bool = True, scale=None):
     """fa_fwd_prefix: q, o [total_q, Hq, D], k, v [total_k, Hkv, D], k_prefix,
     v_prefix [P, Hkv, D], lse [Hq, total_q]."""
-    pr = _prefix_problem(q, k, k_prefix, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k,
-                         causal, scale)
+    pr = _prefix_problem(q, k, v, k_prefix, v_prefix, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
+                         max_seqlen_k, causal, scale)
     _like(q, o)
-    _like(k, v)
-    _like(k_prefix, v_prefix)
     _lse_like(q, lse)
-    if k.dtype != q.dtype or k_prefix.dtype != q.dtype or k.device != q.device \
-            or k_prefix.device != q.device:
-        raise ValueError("all tensors must share dtype and device")
-    _call(load_library().fa_fwd_prefix, "fa_fwd_prefix", q.get_device(), pr, k_prefix.shape[0],
-          *_addr(q, k_prefix, v_prefix, k, v, o), lse.data_ptr())
+    _fwd_prefix(pr, q, k, v, k_prefix, v_prefix, o, lse)
 
 
 def bwd_prefix(q, k, v, k_prefix, v_prefix, do, lse, delta, dq, dk, dv, dk_prefix, dv_prefix,
@@ -1043,40 +1061,42 @@ def bwd_prefix(q, k, v, k_prefix, v_prefix, do, lse, delta, dq, dk, dv, dk_prefi
                scale=None):
     """fa_bwd_prefix: the gradients of fwd_prefix from its lse and delta =
     rowsum(do * o), [Hq, total_q]."""
-    pr = _prefix_problem(q, k, k_prefix, cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k,
-                         causal, scale)
+    pr = _prefix_problem(q, k, v, k_prefix, v_prefix, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
+                         max_seqlen_k, causal, scale)
     _like(q, do, dq)
-    _like(k, v, dk, dv)
-    _like(k_prefix, v_prefix, dk_prefix, dv_prefix)
+    _like(k, dk, dv)
+    _like(k_prefix, dk_prefix, dv_prefix)
     _lse_like(q, lse, delta)
-    if k.dtype != q.dtype or k_prefix.dtype != q.dtype or k.device != q.device \
-            or k_prefix.device != q.device:
-        raise ValueError("all tensors must share dtype and device")
-    _call(load_library().fa_bwd_prefix, "fa_bwd_prefix", q.get_device(), pr, k_prefix.shape[0],
-          *_addr(q, k_prefix, v_prefix, k, v, do), lse.data_ptr(), delta.data_ptr(),
-          *_addr(dq, dk_prefix, dv_prefix, dk, dv))
+    _bwd_prefix(pr, q, k, v, k_prefix, v_prefix, do, lse, delta, dq, dk, dv, dk_prefix, dv_prefix)
 
 
 def attention_prefix_fwd(q, k, v, k_prefix, v_prefix, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
                          max_seqlen_k, causal: bool = True, scale=None):
     """Allocating fwd_prefix: (o, lse)."""
+    pr = _prefix_problem(q, k, v, k_prefix, v_prefix, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
+                         max_seqlen_k, causal, scale)
     o = torch.empty_like(q, memory_format=torch.contiguous_format)
-    lse = torch.empty(q.shape[1], q.shape[0], dtype=torch.float32, device=q.device)
-    fwd_prefix(q, k, v, k_prefix, v_prefix, o, lse, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
-               max_seqlen_k, causal, scale)
+    lse = torch.empty((q.shape[1], q.shape[0]), dtype=torch.float32, device=q.device)
+    _fwd_prefix(pr, q, k, v, k_prefix, v_prefix, o, lse)
     return o, lse
 
 
 def attention_prefix_bwd(q, k, v, k_prefix, v_prefix, o, lse, do, cu_seqlens_q, cu_seqlens_k,
                          max_seqlen_q, max_seqlen_k, causal: bool = True, scale=None):
     """Allocating bwd_prefix: (dq, dk, dv, dk_prefix, dv_prefix)."""
+    pr = _prefix_problem(q, k, v, k_prefix, v_prefix, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
+                         max_seqlen_k, causal, scale)
+    _like(q, o, do)
+    _lse_like(q, lse)
+    total, Hq, D = q.shape
     delta = torch.empty_like(lse)
-    bwd_preprocess(_as4(o, True), _as4(do, True), delta)
-    dq, dk, dv, dkp, dvp = (torch.empty_like(t, memory_format=torch.contiguous_format)
-                            for t in (q, k, v, k_prefix, v_prefix))
-    bwd_prefix(q, k, v, k_prefix, v_prefix, do, lse, delta, dq, dk, dv, dkp, dvp, cu_seqlens_q,
-               cu_seqlens_k, max_seqlen_q, max_seqlen_k, causal, scale)
-    return dq, dk, dv, dkp, dvp
+    _call(load_library().fa_bwd_preprocess, "fa_bwd_preprocess", q.get_device(), o.data_ptr(),
+          do.data_ptr(), delta.data_ptr(), 1, Hq, total, D, _strides4(o), _strides4(do),
+          _DTYPE_CODE[q.dtype])
+    grads = [torch.empty_like(t, memory_format=torch.contiguous_format)
+             for t in (q, k, v, k_prefix, v_prefix)]
+    _bwd_prefix(pr, q, k, v, k_prefix, v_prefix, do, lse, delta, *grads)
+    return tuple(grads)
 
 
 class _AttentionPrefix(torch.autograd.Function):
