@@ -56,8 +56,8 @@ struct PreCfg {
   static constexpr int OFF_RING = 2 * TILE;
   // partial sums are staged over the ring: 2 x 128 rows x D fp32
   static constexpr int RING = NS * TILE > 2 * 128 * D * 4 ? NS * TILE : 2 * 128 * D * 4;
-  static constexpr int OFF_ML = OFF_RING + RING;    // (m, l) of group 1's rows (at first: row offsets)
-  static constexpr int OFF_BAR = OFF_ML + 2048;
+  static constexpr int OFF_ML = OFF_RING + RING;    // (m, l) of group 1's rows
+  static constexpr int OFF_BAR = OFF_ML + 1024;
   static constexpr int SMEM = OFF_BAR + 512 + 1024;
   static constexpr uint32_t COL_S0 = 0, COL_O0 = 256;
 };
@@ -167,6 +167,41 @@ __global__ void __launch_bounds__(320, 1)
     tmem_alloc(smem_u32(&ctl->tmem_base), 512);
     tmem_relinquish();
   }
+  if (warp < 8) {
+    // Query rows gathered into the operand layout of a 128-byte-swizzled load,
+    // while warp 8 sets up; columns past a narrow head dimension are zero, rows
+    // past R hold whatever was there (their results are not used).  A thread
+    // takes one 16-byte unit of every RPP-th row, all its loads at once (with a
+    // division and a load per piece in turn the gather took 10 us of a block):
+    // it finds the place of the rows by one division each, shared by the warp.
+    constexpr int UN = D / 8, RPP = 256 / UN;         // units per row, rows per pass
+    constexpr int PASS = 128 / RPP;                   // passes over one row tile
+    const int nr = nrows[0] + (two ? nrows[1] : 0);
+    const int un = threadIdx.x % UN, rt = threadIdx.x / UN;
+    const bool col = 8 * un < a.dreal;
+    const T* qh = static_cast<const T*>(a.q) + static_cast<int64_t>(hk) * a.G * a.sq[1] + 8 * un;
+#pragma unroll
+    for (int tile = 0; tile < 2; ++tile) {
+      if (tile == 1 && !two) break;
+      uint4 x[PASS];
+#pragma unroll
+      for (int i = 0; i < PASS; ++i) {
+        const int rr = 128 * tile + rt + i * RPP, row = row0 + rr;
+        x[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (rr < nr && col) {
+          const int b = row / a.GN, rem = row - b * a.GN, hg = rem / a.Nq, tok = rem - hg * a.Nq;
+          x[i] = __ldg(reinterpret_cast<const uint4*>(qh + b * a.sq[0] + hg * a.sq[1] + tok * a.sq[2]));
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < PASS; ++i) {
+        const int r = rt + i * RPP;
+        if (128 * tile + r < nr)
+          *reinterpret_cast<uint4*>(sQ + tile * C::TILE + (un >> 3) * C::CHUNK + r * 128 +
+                                    (((un & 7) ^ (r & 7)) << 4)) = x[i];
+      }
+    }
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -270,43 +305,9 @@ __global__ void __launch_bounds__(320, 1)
     __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax + epilogue
-    // Query rows gathered into the operand layout of a 128-byte-swizzled load;
-    // columns past a narrow head dimension are zero, rows past R hold whatever
-    // was there (their results are not used).  Each thread finds one row's
-    // place, then loads eight pieces at a time: with a division and a load per
-    // piece in turn the gather alone took 10 us of a block.
-    {
-      int64_t* sRow = reinterpret_cast<int64_t*>(smem + C::OFF_ML);   // (m, l) come later
-      const int nr = nrows[0] + (two ? nrows[1] : 0);
-      if (static_cast<int>(threadIdx.x) < nr) {
-        const int row = row0 + static_cast<int>(threadIdx.x);
-        const int b = row / a.GN, rem = row - b * a.GN, hg = rem / a.Nq, tok = rem - hg * a.Nq;
-        sRow[threadIdx.x] = b * a.sq[0] + static_cast<int64_t>(hk * a.G + hg) * a.sq[1] + tok * a.sq[2];
-      }
-      bar_red_and(1, 256, true);
-      constexpr int UN = D / 8, RPP = 256 / UN;       // 16-byte units per row, rows per pass
-      const int un = threadIdx.x % UN, rt = threadIdx.x / UN;
-      const bool col = 8 * un < a.dreal;
-      for (int r0 = rt; r0 < nr; r0 += 8 * RPP) {
-        uint4 x[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int r = r0 + i * RPP;
-          x[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (r < nr && col)
-            x[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(a.q) + sRow[r] + 8 * un));
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int rr = r0 + i * RPP, r = rr & 127;
-          if (rr < nr)
-            *reinterpret_cast<uint4*>(sQ + (rr >> 7) * C::TILE + (un >> 3) * C::CHUNK + r * 128 +
-                                      (((un & 7) ^ (r & 7)) << 4)) = x[i];
-        }
-      }
-      fence_async_smem();
-      mbar_arrive(b_q);
-    }
+    // (the query rows were gathered before the sync)
+    fence_async_smem();
+    mbar_arrive(b_q);
     const int g = warp >> 2, quarter = warp & 3;
     const int r = quarter * 32 + lane;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
@@ -459,6 +460,7 @@ __global__ void __launch_bounds__(320, 1)
     if (bar_red_and(1, 256, ok)) {
       const int units = a.dreal / 4;                  // 16-byte units of a partial row
       const int total = nrows[0] + (two ? nrows[1] : 0);   // group 0's rows are full when both have some
+#pragma unroll 4
       for (int idx = threadIdx.x; idx < total * units; idx += 256) {
         const int rr = idx / units, un = idx - rr * units;
         const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(sRing) +
@@ -587,13 +589,21 @@ __global__ void __launch_bounds__(kOwnThreads, own_blocks(D, NT))
     // last leaves the GPU idle around it (a fifth of the time at 128 requests of
     // 1 to 1024 rows).  So block b takes the request of rank b by falling
     // length, which the threads find by counting.
-    __shared__ int sLen[kMaxSorted], sB;
-    for (int i = threadIdx.x; i < a.B; i += kOwnThreads) sLen[i] = __ldg(a.lens + i);
+    __shared__ __align__(16) int sLen[kMaxSorted];
+    __shared__ int sB;
+    for (int i = threadIdx.x; i < kMaxSorted; i += kOwnThreads)
+      sLen[i] = i < a.B ? __ldg(a.lens + i) : INT32_MIN;     // counts before nobody
     __syncthreads();
     for (int i = threadIdx.x; i < a.B; i += kOwnThreads) {
       const int mine = sLen[i];
       int before = 0;
-      for (int j = 0; j < a.B; ++j) before += sLen[j] > mine || (sLen[j] == mine && j < i);
+#pragma unroll 4
+      for (int j = 0; j < a.B; j += 4) {
+        const int4 n = *reinterpret_cast<const int4*>(sLen + j);
+        // of equal lengths the lower index comes first
+        before += (n.x > mine || (n.x == mine && j < i)) + (n.y > mine || (n.y == mine && j + 1 < i)) +
+                  (n.z > mine || (n.z == mine && j + 2 < i)) + (n.w > mine || (n.w == mine && j + 3 < i));
+      }
       if (before == b) sB = i;
     }
     __syncthreads();
