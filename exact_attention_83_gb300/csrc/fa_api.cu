@@ -732,10 +732,7 @@ static fa_status check_decode(const fa_decode_problem* pr, DecodeParams* out) {
 size_t fa_decode_workspace_bytes(const fa_decode_problem* prob) {
   DecodeParams p{};
   if (check_decode(prob, &p) != FA_OK) return 0;
-  const PrefixPlan pl = decode_plan(p.B, p.Hkv, p.G * p.Nq, p.D, p.P);
-  // per range of the prefix and query row: D sums and a log-sum-exp
-  return static_cast<size_t>(pl.ns) * static_cast<size_t>(p.Hkv * p.B * p.G * p.Nq) *
-         static_cast<size_t>(p.D + 1) * sizeof(float);
+  return static_cast<size_t>(decode_plan(p.B, p.Hkv, p.G * p.Nq, p.D, p.P, p.S).floats) * sizeof(float);
 }
 
 fa_status fa_decode(const fa_decode_problem* prob, const void* q, const int64_t* sq,

@@ -17,12 +17,11 @@
 //    into `ns` ranges of key tiles, so that few rows still fill the GPU; each
 //    range leaves partial sums in the workspace (fp32).
 //  * own_kernel: a request's own rows are read by its G * Nq query rows alone.
-//    That is bound by HBM at any rate the matrix units run, so its warps load
-//    K and V straight into the registers of m16n8k16 products, 16 bytes per
-//    lane and whole 64- or 128-byte pieces per row, without shared memory, and
-//    sixteen warps per SM keep the loads in flight.  A cluster of up to eight
-//    blocks shares one request's rows when there are few requests.  The same
-//    kernel then joins all partial sums and writes o and L.
+//    That is bound by HBM at any rate the matrix units run, so its warps stream K
+//    and V through rings in shared memory into m16n8k16 products.  Requests with
+//    many rows are cut into chunks; with one chunk per request (the usual case)
+//    the kernel also joins all partial sums and writes o and L, otherwise
+//    join_kernel does.
 //
 // Rows past a request's length are never read: what they hold does not matter.
 
@@ -56,8 +55,8 @@ struct PreCfg {
   static constexpr int OFF_RING = 2 * TILE;
   // partial sums are staged over the ring: 2 x 128 rows x D fp32
   static constexpr int RING = NS * TILE > 2 * 128 * D * 4 ? NS * TILE : 2 * 128 * D * 4;
-  static constexpr int OFF_ML = OFF_RING + RING;    // (m, l) of group 1's rows
-  static constexpr int OFF_BAR = OFF_ML + 1024;
+  static constexpr int OFF_ML = OFF_RING + RING;    // (m, l) of group 1's rows; at first the rows' places
+  static constexpr int OFF_BAR = OFF_ML + 2048;
   static constexpr int SMEM = OFF_BAR + 512 + 1024;
   static constexpr uint32_t COL_S0 = 0, COL_O0 = 256;
 };
@@ -170,36 +169,41 @@ __global__ void __launch_bounds__(320, 1)
   if (warp < 8) {
     // Query rows gathered into the operand layout of a 128-byte-swizzled load,
     // while warp 8 sets up; columns past a narrow head dimension are zero, rows
-    // past R hold whatever was there (their results are not used).  A thread
-    // takes one 16-byte unit of every RPP-th row, all its loads at once (with a
-    // division and a load per piece in turn the gather took 10 us of a block):
-    // it finds the place of the rows by one division each, shared by the warp.
+    // past R hold whatever was there (their results are not used).  Each thread
+    // finds the place of one row, then copies one 16-byte unit of every RPP-th
+    // row with all its loads in flight (divisions and loads in turn took 5.7 us
+    // for two tiles, a third of a short block).
     constexpr int UN = D / 8, RPP = 256 / UN;         // units per row, rows per pass
-    constexpr int PASS = 128 / RPP;                   // passes over one row tile
+    constexpr int PASS = 256 / RPP;                   // passes over two row tiles
     const int nr = nrows[0] + (two ? nrows[1] : 0);
+    int* sRow = reinterpret_cast<int*>(smem + C::OFF_ML);     // b and g, t of a row ((m, l) come later)
+    if (static_cast<int>(threadIdx.x) < nr) {
+      const int row = row0 + static_cast<int>(threadIdx.x), b = row / a.GN, rem = row - b * a.GN;
+      const int hg = rem / a.Nq;
+      sRow[2 * threadIdx.x] = b;
+      sRow[2 * threadIdx.x + 1] = hg * 16 + (rem - hg * a.Nq);          // fewer than 16 tokens
+    }
+    bar_red_and(1, 256, true);
     const int un = threadIdx.x % UN, rt = threadIdx.x / UN;
     const bool col = 8 * un < a.dreal;
     const T* qh = static_cast<const T*>(a.q) + static_cast<int64_t>(hk) * a.G * a.sq[1] + 8 * un;
+    uint4 x[PASS];
 #pragma unroll
-    for (int tile = 0; tile < 2; ++tile) {
-      if (tile == 1 && !two) break;
-      uint4 x[PASS];
-#pragma unroll
-      for (int i = 0; i < PASS; ++i) {
-        const int rr = 128 * tile + rt + i * RPP, row = row0 + rr;
-        x[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (rr < nr && col) {
-          const int b = row / a.GN, rem = row - b * a.GN, hg = rem / a.Nq, tok = rem - hg * a.Nq;
-          x[i] = __ldg(reinterpret_cast<const uint4*>(qh + b * a.sq[0] + hg * a.sq[1] + tok * a.sq[2]));
-        }
+    for (int i = 0; i < PASS; ++i) {
+      const int r = rt + i * RPP;
+      x[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < nr && col) {
+        const int2 at = *reinterpret_cast<const int2*>(sRow + 2 * r);
+        x[i] = __ldg(reinterpret_cast<const uint4*>(qh + at.x * a.sq[0] + (at.y >> 4) * a.sq[1] +
+                                                    (at.y & 15) * a.sq[2]));
       }
+    }
 #pragma unroll
-      for (int i = 0; i < PASS; ++i) {
-        const int r = rt + i * RPP;
-        if (128 * tile + r < nr)
-          *reinterpret_cast<uint4*>(sQ + tile * C::TILE + (un >> 3) * C::CHUNK + r * 128 +
-                                    (((un & 7) ^ (r & 7)) << 4)) = x[i];
-      }
+    for (int i = 0; i < PASS; ++i) {
+      const int rr = rt + i * RPP, r = rr & 127;
+      if (rr < nr)
+        *reinterpret_cast<uint4*>(sQ + (rr >> 7) * C::TILE + (un >> 3) * C::CHUNK + r * 128 +
+                                  (((un & 7) ^ (r & 7)) << 4)) = x[i];
     }
   }
   tc_fence_before();
@@ -458,14 +462,23 @@ __global__ void __launch_bounds__(320, 1)
         a.part_l[prow0 + row0 + (two ? 128 * g : 0) + r] = m + log2f(l);
     }
     if (bar_red_and(1, 256, ok)) {
-      const int units = a.dreal / 4;                  // 16-byte units of a partial row
-      const int total = nrows[0] + (two ? nrows[1] : 0);   // group 0's rows are full when both have some
-#pragma unroll 4
-      for (int idx = threadIdx.x; idx < total * units; idx += 256) {
-        const int rr = idx / units, un = idx - rr * units;
-        const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(sRing) +
-                                                          rr * D + 4 * (un ^ (rr & 7)));
-        *reinterpret_cast<float4*>(a.part_o + (prow0 + row0 + rr) * a.dreal + 4 * un) = x;
+      // dreal / 4 16-byte units of a partial row (a power of two), eight loads of
+      // the staged rows before their stores
+      const int sh = 31 - __clz(a.dreal / 4), total = nrows[0] + (two ? nrows[1] : 0);
+      float4* dst = reinterpret_cast<float4*>(a.part_o + (prow0 + row0) * a.dreal);
+      const int n16 = total << sh;                    // group 0's rows are full when both have some
+      for (int i0 = threadIdx.x; i0 < n16; i0 += 8 * 256) {
+        float4 x[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const int idx = i0 + 256 * i, rr = idx >> sh, un = idx & ((1 << sh) - 1);
+          if (idx < n16)
+            x[i] = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(sRing) + rr * D +
+                                                    4 * (un ^ (rr & 7)));
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          if (i0 + 256 * i < n16) dst[i0 + 256 * i] = x[i];
       }
     }
   }
@@ -479,28 +492,40 @@ __global__ void __launch_bounds__(320, 1)
 }
 
 // ============================================================================
-// Own rows, and the join
+// Own rows
 // ============================================================================
-// A block of four warps takes 8 NT query rows of one (request, key/value
-// head); warp w of block `rank` of the cluster takes every (4 * cluster)-th
-// block of 16 keys.  Scores are formed transposed, S^T = K Q^T, and so is the
-// output, O^T = V^T P^T: the keys (then the columns of V) fill the 16 rows of
-// the m16n8k16 products and the few query rows their 8 columns, so that no
-// half of a product is padding for up to eight query rows and the sums take
-// D / 4 registers per lane and tile.
+// A block of four warps takes 8 NT query rows of one (request, key/value head)
+// and one chunk of the request's rows; warp w takes every fourth block of 16
+// keys.  Scores are formed transposed, S^T = K Q^T, and so is the output,
+// O^T = V^T P^T: the keys (then the columns of V) fill the 16 rows of the
+// m16n8k16 products and the few query rows their 8 columns, so that no half of
+// a product is padding for up to eight query rows and the sums take D / 4
+// registers per lane and tile.
+// Each warp copies its own blocks of keys into a ring in shared memory, ahead of
+// its work (cp.async, 512 contiguous bytes per instruction, no barrier between
+// warps): what has to be in flight to keep HBM busy, some 100 KB per SM, is more
+// than registers hold (loads into the products' registers, half of them empty at
+// any time, took 53.9 us where the rings take 45.8).  Blocks that walk several
+// requests with their rings running ahead were no faster: the joins between them
+// take longer than a ring covers.
 // Lane 4 g + c holds, of an operand with rows g and g + 8, the elements in
 // slots 2c, 2c+1, 2c+8, 2c+9 of 16.  The order of a contraction is free, so the
 // slots of two products over K take the eight elements 8c .. 8c+7 of a
-// 32-element piece: one 16-byte load.  Of V the lane holds keys 2c, 2c+1, 2c+8,
+// 32-element piece: one 16-byte read.  Of V the lane holds keys 2c, 2c+1, 2c+8,
 // 2c+9; product tile j takes as its rows g and g + 8 the elements 8g + 2j and
-// 8g + 2j + 1 of a 64-element piece, so four tiles share one 16-byte load of
+// 8g + 2j + 1 of a 64-element piece, so four tiles share one 16-byte read of
 // each of the four keys.  P^T comes out of S^T with its halves the other way
-// round; movmatrix turns them.
+// round; movmatrix turns them.  16-byte unit u of row r lies at unit
+// u ^ 4 (r mod 2) of its row for K and u ^ 2 (r / 2 mod 4) for V, which spreads
+// the eight reads of a quarter of a warp over all banks.
+// With one chunk per request the block also joins its sums with the prefix's and
+// writes o and L; otherwise it leaves its sums for join_kernel.
 constexpr int kOwnThreads = 128;
 constexpr int kOwnWarps = kOwnThreads / 32;
-constexpr int kMaxCluster = 8;
 constexpr int kMaxRanges = 64;            // ranges of the prefix
+constexpr int kMaxChunks = 64;            // chunks of a request's own rows
 constexpr int kMaxSorted = 256;           // requests that a block ranks by length
+constexpr int kDeepRows = 1024;           // rows per block above which deep rings pay (OwnCfg)
 
 struct OwnArgs {
   const void* q; const void* k; const void* v;
@@ -512,11 +537,14 @@ struct OwnArgs {
   int B, Hq, Hkv, G, Nq, GN, RT;     // RT: tiles of 8 NT of the GN rows
   int dreal, causal;
   float c;
-  int cluster;
   int longest_first;                 // blocks take the requests by falling length
+  float len_scale;                   // 2^22 / (S + 1)
+  int chunks, chunk;                 // chunks of `chunk` rows (a multiple of 64) per request
   int ns, R;                         // prefix partial sums (ns = 0: none)
-  const float* part_o;
-  const float* part_l;
+  const float* part_o;               // [Hkv][ns][R][dreal]
+  const float* part_l;               // [Hkv][ns][R]
+  float* own_o;                      // [Hkv][chunks][R][dreal]; chunks > 1
+  float* own_l;                      // [Hkv][chunks][R]
   unsigned int* status;
 };
 
@@ -543,9 +571,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 
-__device__ __forceinline__ uint4 ld_stream(const void* p) {
-  return __ldcs(static_cast<const uint4*>(p));
-}
 __device__ __forceinline__ uint32_t word(const uint4& v, int i) {
   return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
@@ -561,25 +586,41 @@ __device__ __forceinline__ float sum_g(float v) {
   return v + __shfl_xor_sync(0xffffffffu, v, 16);
 }
 
-// Blocks per SM that the registers are kept to.
-constexpr int own_blocks(int D, int NT) {
-  return D == 64 ? (NT == 1 ? 4 : 3) : (NT == 1 ? 3 : 2);
-}
+// Shared memory of a block: per warp a ring of K | V blocks of 16 rows, over
+// which its sums are laid at the end.
+// Two shapes.  Deep rings (three blocks of rows, four at D = 64; two blocks of
+// threads per SM, three) keep more in flight; shallow ones (one block of rows
+// less, one block of threads more) hide more of the blocks' starts and joins.
+// Own rows alone, D = 128, 8 heads: 128 requests of up to 1024 rows 56.0 us deep,
+// 51.8 shallow; 64 of up to 2048 45.8 and 51.9 (5.9 TB/s of the 6.8 that a copy
+// reaches); D = 64, 16 of up to 8192 in chunks 37.5 and 43.7.
+template <int D, int NT, bool DEEP>
+struct OwnCfg {
+  static constexpr int STAGES = (D == 128 ? 3 : 4) - (DEEP ? 0 : 1);
+  static constexpr int KV = 16 * D * 2;               // bytes of 16 rows of K or V
+  static constexpr int RING = STAGES * 2 * KV;        // per warp
+  static constexpr int SMEM = kOwnWarps * RING;
+  static constexpr int BLOCKS = (D == 128 ? 3 : 4) - (DEEP || NT == 2 ? 1 : 0);     // per SM
+  static_assert(8 * NT * D * 4 <= RING, "a warp's sums fit its ring");
+};
 
-template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kOwnThreads, own_blocks(D, NT))
+template <typename T, int D, int NT, bool DEEP>
+__global__ void __launch_bounds__(kOwnThreads, (OwnCfg<D, NT, DEEP>::BLOCKS))
     own_kernel(const __grid_constant__ OwnArgs a) {
+  using C = OwnCfg<D, NT, DEEP>;
   constexpr int KP = D / 32;              // 32-element pieces of a K row
   constexpr int VP = D / 64;              // 64-element pieces of a V row
+  constexpr int UN = D / 8;               // 16-byte units of a row
   constexpr int ROWS = 8 * NT;
-  __shared__ __align__(16) float sO[kOwnWarps][ROWS][D];
+  extern __shared__ __align__(128) uint8_t own_smem[];
   __shared__ float sL[kOwnWarps][ROWS];   // log2 of each warp's sum, -inf: no key
-  __shared__ float sW[ROWS][kOwnWarps * kMaxCluster];
+  __shared__ float sW[ROWS][kOwnWarps];
   __shared__ float sP[ROWS][kMaxRanges];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g8 = lane >> 2, c4 = lane & 3;
-  const int rank = static_cast<int>(blockIdx.x % a.cluster);
-  int id = static_cast<int>(blockIdx.x / a.cluster);
+  int id = static_cast<int>(blockIdx.x);
+  const int ck = id % a.chunks;
+  id /= a.chunks;
   const int rt = id % a.RT;
   id /= a.RT;
   const int hk = id % a.Hkv;
@@ -588,21 +629,24 @@ __global__ void __launch_bounds__(kOwnThreads, own_blocks(D, NT))
     // Blocks start in the order of their index, and a long request that starts
     // last leaves the GPU idle around it (a fifth of the time at 128 requests of
     // 1 to 1024 rows).  So block b takes the request of rank b by falling
-    // length, which the threads find by counting.
-    __shared__ __align__(16) int sLen[kMaxSorted];
+    // length, which the threads find by counting.  One key holds a length (22
+    // bits of it suffice) and, so that no two are alike, the request.
+    __shared__ __align__(16) int sKey[kMaxSorted];
     __shared__ int sB;
-    for (int i = threadIdx.x; i < kMaxSorted; i += kOwnThreads)
-      sLen[i] = i < a.B ? __ldg(a.lens + i) : INT32_MIN;     // counts before nobody
+    auto key_of = [&](int i) {
+      const int n = __ldg(a.lens + i);
+      const float f = static_cast<float>(n < 0 ? 0 : n) * a.len_scale;
+      return static_cast<int>(f < 4194303.f ? f : 4194303.f) * kMaxSorted + (kMaxSorted - 1 - i);
+    };
+    for (int i = threadIdx.x; i < kMaxSorted; i += kOwnThreads) sKey[i] = i < a.B ? key_of(i) : -1;
     __syncthreads();
     for (int i = threadIdx.x; i < a.B; i += kOwnThreads) {
-      const int mine = sLen[i];
+      const int mine = sKey[i];
       int before = 0;
-#pragma unroll 4
+#pragma unroll 8
       for (int j = 0; j < a.B; j += 4) {
-        const int4 n = *reinterpret_cast<const int4*>(sLen + j);
-        // of equal lengths the lower index comes first
-        before += (n.x > mine || (n.x == mine && j < i)) + (n.y > mine || (n.y == mine && j + 1 < i)) +
-                  (n.z > mine || (n.z == mine && j + 2 < i)) + (n.w > mine || (n.w == mine && j + 3 < i));
+        const int4 n = *reinterpret_cast<const int4*>(sKey + j);
+        before += (n.x > mine) + (n.y > mine) + (n.z > mine) + (n.w > mine);
       }
       if (before == b) sB = i;
     }
@@ -610,42 +654,49 @@ __global__ void __launch_bounds__(kOwnThreads, own_blocks(D, NT))
     b = sB;
   }
   const int len = a.lens ? __ldg(a.lens + b) : 0;
-  if (len < 0 || len > a.S) {             // every block of the cluster takes this
-    if (threadIdx.x == 0) record_status(a.status, FA_ERR_SEQLENS);
+  const bool bad = len < 0 || len > a.S;
+  if (bad && threadIdx.x == 0) record_status(a.status, FA_ERR_SEQLENS);
+  const int key_from = ck * a.chunk;
+  if (bad || (a.chunks > 1 && key_from >= len)) {      // nothing to leave: join_kernel knows the length
     asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
   }
+  const int key_to = len - key_from < a.chunk ? len : key_from + a.chunk;
   const int r0 = rt * ROWS;
   const int nr = a.GN - r0 < ROWS ? a.GN - r0 : ROWS;      // valid rows
 
-  const T* kbase = static_cast<const T*>(a.k) + b * a.sk[0] + hk * a.sk[1] + 8 * c4;
-  const T* vbase = static_cast<const T*>(a.v) + b * a.sv[0] + hk * a.sv[1] + 8 * g8;
-  const int stride = 16 * kOwnWarps * a.cluster;
-  uint4 kr[2][KP], vr[4][VP];
-  auto load_k = [&](int key0) {
+  uint8_t* ring = own_smem + warp * C::RING;
+  // This lane's units of a block: unit lane % UN of rows lane / UN, + 32 / UN, ...
+  const int un = lane % UN, row_l = lane / UN;
+  const bool col = 8 * un < a.dreal;
+  const T* kbase = static_cast<const T*>(a.k) + b * a.sk[0] + hk * a.sk[1] + 8 * un;
+  const T* vbase = static_cast<const T*>(a.v) + b * a.sv[0] + hk * a.sv[1] + 8 * un;
+  const uint32_t ring_s = smem_u32(ring);
+  constexpr int STRIDE = 16 * kOwnWarps;
+  const int first = key_from + warp * 16;
+  auto copy = [&](int key0, int stage) {
+    if (key0 < key_to) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int key = key0 + 8 * t + g8;
-      const T* row = kbase + key * a.sk[2];
-#pragma unroll
-      for (int p = 0; p < KP; ++p)
-        kr[t][p] = key < len && 32 * p + 8 * c4 < a.dreal ? ld_stream(row + 32 * p)
-                                                          : make_uint4(0u, 0u, 0u, 0u);
+      for (int i = 0; i < 16 * UN / 32; ++i) {
+        const int r = row_l + i * (32 / UN), key = key0 + r;
+        const bool on = col && key < key_to;
+        // rows past the length are not read; the copy of 0 bytes fills zeros
+        const T* ks = on ? kbase + key * a.sk[2] : kbase;
+        const T* vs = on ? vbase + key * a.sv[2] : vbase;
+        const uint32_t dst = ring_s + stage * 2 * C::KV + r * (D * 2);
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + ((un ^ (4 * (r & 1))) << 4)),
+                     "l"(ks), "r"(on ? 16 : 0)
+                     : "memory");
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + C::KV +
+                                                                          ((un ^ (2 * ((r >> 1) & 3))) << 4)),
+                     "l"(vs), "r"(on ? 16 : 0)
+                     : "memory");
+      }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  auto load_v = [&](int key0) {
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const int key = key0 + 2 * c4 + (t & 1) + 8 * (t >> 1);
-      const T* row = vbase + key * a.sv[2];
-#pragma unroll
-      for (int p = 0; p < VP; ++p)
-        vr[t][p] = key < len && 64 * p + 8 * g8 < a.dreal ? ld_stream(row + 64 * p)
-                                                          : make_uint4(0u, 0u, 0u, 0u);
-    }
-  };
-  const int first = (rank * kOwnWarps + warp) * 16;
-  if (first < len) load_k(first);
+  for (int i = 0; i < C::STAGES - 1; ++i) copy(first + i * STRIDE, i);
   // Query rows as the second operand: row 8 nt + g, the same pieces as K's
   uint4 qr[NT][KP];
 #pragma unroll
@@ -678,19 +729,28 @@ __global__ void __launch_bounds__(kOwnThreads, own_blocks(D, NT))
     l[nt][0] = l[nt][1] = 0.f;
   }
 
-  for (int key0 = first; key0 < len; key0 += stride) {
-    load_v(key0);
+  int stage = 0;
+  for (int key0 = first; key0 < key_to; key0 += STRIDE) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(C::STAGES - 2) : "memory");
+    __syncwarp();                          // every lane's copies; the last block is no longer read
+    copy(key0 + (C::STAGES - 1) * STRIDE, stage == 0 ? C::STAGES - 1 : stage - 1);
+    const uint8_t* ks = ring + stage * 2 * C::KV;
+    const uint8_t* vs = ks + C::KV;
+    stage = stage + 1 == C::STAGES ? 0 : stage + 1;
     float s[NT][4];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
+    for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.f;
 #pragma unroll
-      for (int p = 0; p < KP; ++p) {
-        mma16816<T>(s[nt], kr[0][p].x, kr[1][p].x, kr[0][p].y, kr[1][p].y, qr[nt][p].x, qr[nt][p].y);
-        mma16816<T>(s[nt], kr[0][p].z, kr[1][p].z, kr[0][p].w, kr[1][p].w, qr[nt][p].z, qr[nt][p].w);
+    for (int p = 0; p < KP; ++p) {
+      const int at = ((4 * p + c4) ^ (4 * (g8 & 1))) << 4;      // rows g and g + 8 swap alike
+      const uint4 k0 = *reinterpret_cast<const uint4*>(ks + g8 * (D * 2) + at);
+      const uint4 k1 = *reinterpret_cast<const uint4*>(ks + (g8 + 8) * (D * 2) + at);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        mma16816<T>(s[nt], k0.x, k1.x, k0.y, k1.y, qr[nt][p].x, qr[nt][p].y);
+        mma16816<T>(s[nt], k0.z, k1.z, k0.w, k1.w, qr[nt][p].z, qr[nt][p].w);
       }
     }
-    if (key0 < len - stride) load_k(key0 + stride);
     uint32_t pb[NT][2];
     float alpha[NT][2];
     bool moved = false;
@@ -701,8 +761,10 @@ __global__ void __launch_bounds__(kOwnThreads, own_blocks(D, NT))
       for (int e = 0; e < 2; ++e) {
         float x[2];
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-          x[t] = key0 + 8 * t + g8 <= lim[nt][e] ? s[nt][2 * t + e] * a.c : -INFINITY;
+        for (int t = 0; t < 2; ++t) {
+          const int key = key0 + 8 * t + g8;
+          x[t] = key <= lim[nt][e] && key < key_to ? s[nt][2 * t + e] * a.c : -INFINITY;
+        }
         const float mn = fmaxf(m[nt][e], max_g(fmaxf(x[0], x[1])));
         // no key seen yet: exponents against 0, so that -inf stays a weight of 0
         const float ms = mn == -INFINITY ? 0.f : mn;
@@ -729,19 +791,27 @@ __global__ void __launch_bounds__(kOwnThreads, own_blocks(D, NT))
         }
     }
 #pragma unroll
-    for (int p = 0; p < VP; ++p)
+    for (int p = 0; p < VP; ++p) {
+      uint4 vr[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {        // keys 2 c4 + {0, 1} + {0, 8}: r / 2 mod 4 = c4
+        const int r = 2 * c4 + (t & 1) + 8 * (t >> 1);
+        vr[t] = *reinterpret_cast<const uint4*>(vs + r * (D * 2) + (((8 * p + g8) ^ (2 * c4)) << 4));
+      }
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const uint32_t v0 = word(vr[0][p], j), v1 = word(vr[1][p], j), v2 = word(vr[2][p], j),
-                       v3 = word(vr[3][p], j);
+        const uint32_t v0 = word(vr[0], j), v1 = word(vr[1], j), v2 = word(vr[2], j), v3 = word(vr[3], j);
         const uint32_t a0 = prmt(v0, v1, 0x5410u), a1 = prmt(v0, v1, 0x7632u),
                        a2 = prmt(v2, v3, 0x5410u), a3 = prmt(v2, v3, 0x7632u);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
           mma16816<T>(o[4 * p + j][nt], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
       }
+    }
   }
-  // This warp's sums, normalised, with log2 of the sum of exponentials
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncwarp();                            // the ring is done with: the warp's sums go over it
+  float* sO = reinterpret_cast<float*>(ring);             // [ROWS][D]
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -753,38 +823,31 @@ __global__ void __launch_bounds__(kOwnThreads, own_blocks(D, NT))
       if (g8 == 0) sL[warp][row] = none ? -INFINITY : m[nt][e] + log2f(ls);
 #pragma unroll
       for (int p = 0; p < VP; ++p) {
-        float4* dst = reinterpret_cast<float4*>(&sO[warp][row][64 * p + 8 * g8]);
+        float4* dst = reinterpret_cast<float4*>(sO + row * D + 64 * p + 8 * g8);
 #pragma unroll
         for (int j = 0; j < 4; j += 2)
           dst[j / 2] = make_float4(o[4 * p + j][nt][e] * inv, o[4 * p + j][nt][2 + e] * inv,
                                    o[4 * p + j + 1][nt][e] * inv, o[4 * p + j + 1][nt][2 + e] * inv);
       }
     }
-  if (a.cluster > 1) cluster_sync_all();
-  else __syncthreads();
+  __syncthreads();
   // the prefix's partial sums are complete and visible from here on
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  // Join: per row, the weights of every piece; warp w takes rows w, w + 4, ...
-  const int pieces = kOwnWarps * a.cluster;
+  // Per row, the weights of the four warps' sums and, when this is the only
+  // chunk, of the prefix's; warp w takes rows w, w + 4, ...
+  const int ns = a.chunks == 1 ? a.ns : 0;
   const int64_t prow = static_cast<int64_t>(b) * a.GN + r0;    // row within the head's R rows
   const float* pl = a.part_l + static_cast<int64_t>(hk) * a.ns * a.R + prow;
+  const int64_t orow = (static_cast<int64_t>(hk) * a.chunks + ck) * a.R + prow;
   for (int row = warp; row < nr; row += kOwnWarps) {
-    float own = -INFINITY;                 // piece `lane` of the own rows (at most 32)
-    if (lane < pieces) {
-      const uint32_t at = smem_u32(&sL[lane % kOwnWarps][row]);
-      if (a.cluster > 1)
-        asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                     : "=f"(own) : "r"(cluster_map(at, static_cast<uint32_t>(lane / kOwnWarps))) : "memory");
-      else
-        own = sL[lane][row];
-    }
+    const float own = lane < kOwnWarps ? sL[lane][row] : -INFINITY;
     float pre[kMaxRanges / 32];            // ranges lane, lane + 32 of the prefix
     float mx = own;
 #pragma unroll
     for (int i = 0; i < kMaxRanges / 32; ++i) {
       const int rg = lane + 32 * i;
-      pre[i] = rg < a.ns ? __ldg(pl + static_cast<int64_t>(rg) * a.R + row) : -INFINITY;
+      pre[i] = rg < ns ? __ldg(pl + static_cast<int64_t>(rg) * a.R + row) : -INFINITY;
       mx = fmaxf(mx, pre[i]);
     }
 #pragma unroll
@@ -797,53 +860,118 @@ __global__ void __launch_bounds__(kOwnThreads, own_blocks(D, NT))
     for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
     const float L2 = mx == -INFINITY ? -INFINITY : ms + log2f(sum);
     const float Lw = mx == -INFINITY ? 0.f : L2;
-    if (lane < pieces) sW[row][lane] = ex2(own - Lw);
+    if (lane < kOwnWarps) sW[row][lane] = ex2(own - Lw);
 #pragma unroll
     for (int i = 0; i < kMaxRanges / 32; ++i)
-      if (lane + 32 * i < a.ns) sP[row][lane + 32 * i] = ex2(pre[i] - Lw);
-    if (lane == 0 && rank == 0) {
-      const int gr = r0 + row, hg = gr / a.Nq, tok = gr - hg * a.Nq;
-      a.lse[(static_cast<int64_t>(b) * a.Hq + hk * a.G + hg) * a.Nq + tok] = L2 * kLn2;
+      if (lane + 32 * i < ns) sP[row][lane + 32 * i] = ex2(pre[i] - Lw);
+    if (lane == 0) {
+      if (a.chunks > 1) {
+        a.own_l[orow + row] = L2;
+      } else {
+        const int gr = r0 + row, hg = gr / a.Nq, tok = gr - hg * a.Nq;
+        a.lse[(static_cast<int64_t>(b) * a.Hq + hk * a.G + hg) * a.Nq + tok] = L2 * kLn2;
+      }
     }
   }
   __syncthreads();
   const int units = a.dreal / 4;
-  for (int idx = threadIdx.x + kOwnThreads * rank; idx < nr * units; idx += kOwnThreads * a.cluster) {
-    const int row = idx / units, un = idx - row * units;
+  for (int idx = threadIdx.x; idx < nr * units; idx += kOwnThreads) {
+    const int row = idx / units, u4 = idx - row * units;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     auto add = [&](float w, const float4& x) {
       acc.x = fmaf(w, x.x, acc.x); acc.y = fmaf(w, x.y, acc.y);
       acc.z = fmaf(w, x.z, acc.z); acc.w = fmaf(w, x.w, acc.w);
     };
-    const float* po = a.part_o + (static_cast<int64_t>(hk) * a.ns * a.R + prow + row) * a.dreal + 4 * un;
+    const float* po = a.part_o + (static_cast<int64_t>(hk) * a.ns * a.R + prow + row) * a.dreal + 4 * u4;
     const int64_t step = static_cast<int64_t>(a.R) * a.dreal;
     int i = 0;
-    for (; i + 8 <= a.ns; i += 8) {          // eight loads in flight
+    for (; i + 8 <= ns; i += 8) {            // eight loads in flight
       float4 x[8];
 #pragma unroll
       for (int t = 0; t < 8; ++t) x[t] = __ldg(reinterpret_cast<const float4*>(po + (i + t) * step));
 #pragma unroll
       for (int t = 0; t < 8; ++t) add(sP[row][i + t], x[t]);
     }
-    for (; i < a.ns; ++i) add(sP[row][i], __ldg(reinterpret_cast<const float4*>(po + i * step)));
-    for (int rk = 0; rk < a.cluster; ++rk)
+    for (; i < ns; ++i) add(sP[row][i], __ldg(reinterpret_cast<const float4*>(po + i * step)));
 #pragma unroll
-      for (int w = 0; w < kOwnWarps; ++w) {
-        const float4 x = a.cluster > 1
-                             ? ld_cluster_f4(cluster_map(smem_u32(&sO[w][row][4 * un]), static_cast<uint32_t>(rk)))
-                             : *reinterpret_cast<const float4*>(&sO[w][row][4 * un]);
-        add(sW[row][rk * kOwnWarps + w], x);
-      }
-    const int gr = r0 + row, hg = gr / a.Nq, tok = gr - hg * a.Nq;
-    T* dst = static_cast<T*>(a.o) + b * a.so[0] + static_cast<int64_t>(hk * a.G + hg) * a.so[1] +
-             tok * a.so[2] + 4 * un;
-    uint2 w2;
-    w2.x = pack2<T>(acc.x, acc.y);
-    w2.y = pack2<T>(acc.z, acc.w);
-    *reinterpret_cast<uint2*>(dst) = w2;
+    for (int w = 0; w < kOwnWarps; ++w)
+      add(sW[row][w], *reinterpret_cast<const float4*>(own_smem + w * C::RING + (row * D + 4 * u4) * 4));
+    if (a.chunks > 1) {
+      *reinterpret_cast<float4*>(a.own_o + (orow + row) * a.dreal + 4 * u4) = acc;
+    } else {
+      const int gr = r0 + row, hg = gr / a.Nq, tok = gr - hg * a.Nq;
+      T* dst = static_cast<T*>(a.o) + b * a.so[0] + static_cast<int64_t>(hk * a.G + hg) * a.so[1] +
+               tok * a.so[2] + 4 * u4;
+      *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<T>(acc.x, acc.y), pack2<T>(acc.z, acc.w));
+    }
   }
-  // no block leaves while another still reads its shared memory
-  if (a.cluster > 1) cluster_sync_all();
+}
+
+// ============================================================================
+// The join of several chunks
+// ============================================================================
+// One warp per output row: the log-sum-exps of all its pieces (prefix ranges,
+// then the chunks that the request's length reaches) give their weights, then
+// the lanes add the pieces' sums, dreal / 4 lanes to a piece.
+template <typename T>
+__global__ void __launch_bounds__(kOwnThreads) join_kernel(const __grid_constant__ OwnArgs a) {
+  constexpr int PIECES = kMaxRanges + kMaxChunks;
+  __shared__ float sW[kOwnWarps][PIECES];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kOwnWarps + warp;   // of Hkv * R
+  if (row >= static_cast<int64_t>(a.Hkv) * a.R) return;
+  const int hk = static_cast<int>(row / a.R), r = static_cast<int>(row - static_cast<int64_t>(hk) * a.R);
+  const int b = r / a.GN, gr = r - b * a.GN, hg = gr / a.Nq, tok = gr - hg * a.Nq;
+  const int len = __ldg(a.lens + b);
+  if (len < 0 || len > a.S) return;          // reported by own_kernel
+  const int nc = (len + a.chunk - 1) / a.chunk, n = a.ns + nc;
+  auto piece_l = [&](int i) {
+    return i < a.ns ? a.part_l[(static_cast<int64_t>(hk) * a.ns + i) * a.R + r]
+                    : a.own_l[(static_cast<int64_t>(hk) * a.chunks + i - a.ns) * a.R + r];
+  };
+  float L[PIECES / 32], mx = -INFINITY;
+#pragma unroll
+  for (int i = 0; i < PIECES / 32; ++i) {
+    L[i] = lane + 32 * i < n ? piece_l(lane + 32 * i) : -INFINITY;
+    mx = fmaxf(mx, L[i]);
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+  const float ms = mx == -INFINITY ? 0.f : mx;
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < PIECES / 32; ++i) sum += ex2(L[i] - ms);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  const float L2 = mx == -INFINITY ? -INFINITY : ms + log2f(sum), Lw = mx == -INFINITY ? 0.f : L2;
+#pragma unroll
+  for (int i = 0; i < PIECES / 32; ++i)
+    if (lane + 32 * i < n) sW[warp][lane + 32 * i] = ex2(L[i] - Lw);
+  __syncwarp();
+  const int lpp = a.dreal / 4, grp = lane / lpp, col = lane % lpp, ngrp = 32 / lpp;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int i = grp; i < n; i += ngrp) {
+    const float* src = i < a.ns ? a.part_o + ((static_cast<int64_t>(hk) * a.ns + i) * a.R + r) * a.dreal
+                                : a.own_o + ((static_cast<int64_t>(hk) * a.chunks + i - a.ns) * a.R + r) * a.dreal;
+    const float4 x = *reinterpret_cast<const float4*>(src + 4 * col);
+    const float w = sW[warp][i];
+    acc.x = fmaf(w, x.x, acc.x); acc.y = fmaf(w, x.y, acc.y);
+    acc.z = fmaf(w, x.z, acc.z); acc.w = fmaf(w, x.w, acc.w);
+  }
+  for (int off = lpp; off < 32; off <<= 1) {
+    acc.x += __shfl_xor_sync(0xffffffffu, acc.x, off);
+    acc.y += __shfl_xor_sync(0xffffffffu, acc.y, off);
+    acc.z += __shfl_xor_sync(0xffffffffu, acc.z, off);
+    acc.w += __shfl_xor_sync(0xffffffffu, acc.w, off);
+  }
+  const int64_t h = hk * a.G + hg;
+  if (grp == 0) {
+    T* dst = static_cast<T*>(a.o) + b * a.so[0] + h * a.so[1] + tok * a.so[2] + 4 * col;
+    *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<T>(acc.x, acc.y), pack2<T>(acc.z, acc.w));
+  }
+  if (lane == 0) a.lse[(static_cast<int64_t>(b) * a.Hq + h) * a.Nq + tok] = L2 * kLn2;
 }
 
 // ----------------------------------------------------------------- host side
@@ -853,35 +981,54 @@ constexpr int kPlanSMs = 152;
 
 // How the prefix is cut.  A block costs a start and an end plus a time per key
 // tile; the ranges' partial sums cost their way through the L2 cache in
-// proportion to their number.  The cheapest number of ranges by that estimate.
-PrefixPlan make_plan(int64_t B, int64_t Hkv, int64_t GN, int64_t D, int64_t P) {
-  PrefixPlan pl{};
-  if (P < 1) return pl;
-  const int64_t R = B * GN, n = (P + 127) / 128;
-  pl.two = R > 128;
-  pl.groups = pl.two ? (R + 255) / 256 : 1;
-  const int64_t base = Hkv * pl.groups;
-  const double per_tile = D > 64 ? 1.5 : 0.8, fixed = 5.0;      // microseconds
-  const double join = static_cast<double>(R) * Hkv * D * 8 / 10e6;  // per range
+// proportion to their number.  The cheapest number of ranges by that estimate
+// (microseconds; a trace of the blocks gave 10 to 12 beside their tiles).
+void plan_prefix(int64_t R, int64_t Hkv, int64_t D, int64_t P, DecodePlan* pl) {
+  const int64_t n = (P + 127) / 128;
+  pl->two = R > 128;
+  pl->groups = pl->two ? (R + 255) / 256 : 1;
+  const int64_t base = Hkv * pl->groups;
+  const double per_tile = D > 64 ? 1.45 : 0.8, fixed = 11.0;
+  const double join = static_cast<double>(R) * static_cast<double>(Hkv * D) * 8 / 10e6;  // per range
   double best = 0;
   const int64_t most = n < kMaxRanges ? n : kMaxRanges;
   for (int64_t ns = 1; ns <= most; ++ns) {
     const double waves = static_cast<double>((base * ns + kPlanSMs - 1) / kPlanSMs);
-    const double t = waves * (fixed + per_tile * static_cast<double>((n + ns - 1) / ns)) + join * ns;
+    const double t = waves * (fixed + per_tile * static_cast<double>((n + ns - 1) / ns)) +
+                     join * static_cast<double>(ns);
     if (ns == 1 || t < best) {
       best = t;
-      pl.ns = static_cast<int>(ns);
+      pl->ns = static_cast<int>(ns);
     }
   }
-  return pl;
 }
+
+// How the own rows are cut: into chunks of 512 rows at least, as long as that
+// gives SMs without a block one, since several chunks cost a further kernel (4 us
+// and more).  4 requests of up to 32768 rows, 8 heads: 65 us in chunks, 80 when a
+// cluster of eight blocks joined its sums through distributed shared memory.
+void plan_own(int64_t base, int64_t D, int64_t S, DecodePlan* pl) {
+  const int64_t slots = static_cast<int64_t>(kPlanSMs) * (D == 128 ? 2 : 3);
+  int64_t c = 1;
+  while (c < kMaxChunks && base * c < slots && S / (2 * c) >= 512) c *= 2;
+  pl->chunk = ((S + c - 1) / c + 63) / 64 * 64;
+  if (pl->chunk < 64) pl->chunk = 64;
+  pl->chunks = static_cast<int>(S > 0 ? (S + pl->chunk - 1) / pl->chunk : 1);
+}
+
+// Query rows of a block of own_kernel: 8, or 16 where a request has more.
+int own_rows(int64_t GN) { return GN <= 8 ? 8 : 16; }
 
 template <typename T, int D>
 fa_status run_decode(const DecodeParams& p, cudaStream_t stream) {
   const int64_t GN = p.G * p.Nq, R = p.B * GN;
-  const PrefixPlan pl = make_plan(p.B, p.Hkv, GN, p.D, p.P);
+  const DecodePlan pl = decode_plan(p.B, p.Hkv, GN, p.D, p.P, p.S);
   float* part_o = p.ws;
-  float* part_l = p.ws + static_cast<int64_t>(pl.ns) * p.Hkv * R * p.D;
+  float* part_l = part_o + static_cast<int64_t>(pl.ns) * p.Hkv * R * p.D;
+  // the log-sum-exps take whole 16-byte units, so that the sums behind them stay aligned
+  const int64_t nl = (static_cast<int64_t>(pl.ns) * p.Hkv * R + 3) / 4 * 4;
+  float* own_o = part_l + nl;
+  float* own_l = own_o + static_cast<int64_t>(pl.chunks) * p.Hkv * R * p.D;
   if (pl.ns > 0) {
     CUtensorMap mk, mv;
     if (!encode_tile_map(&mk, p.kp, p.dtype, 1, p.Hkv, p.P, p.D, p.skp, 128, 64) ||
@@ -915,55 +1062,68 @@ fa_status run_decode(const DecodeParams& p, cudaStream_t stream) {
   a.S = p.S;
   a.B = static_cast<int>(p.B); a.Hq = static_cast<int>(p.Hkv * p.G); a.Hkv = static_cast<int>(p.Hkv);
   a.G = static_cast<int>(p.G); a.Nq = static_cast<int>(p.Nq); a.GN = static_cast<int>(GN);
-  const int NT = GN <= 8 ? 1 : 2;
-  a.RT = static_cast<int>((GN + 8 * NT - 1) / (8 * NT));
+  const int rows = own_rows(GN);
+  a.RT = static_cast<int>((GN + rows - 1) / rows);
   a.dreal = static_cast<int>(p.D); a.causal = p.causal;
   a.c = p.scale * kLog2e;
+  a.chunks = pl.chunks; a.chunk = static_cast<int>(pl.chunk);
   a.ns = pl.ns; a.R = static_cast<int>(R);
-  a.part_o = part_o; a.part_l = part_l;
+  a.part_o = part_o; a.part_l = part_l; a.own_o = own_o; a.own_l = own_l;
   a.status = p.status;
-  const int64_t base = p.B * p.Hkv * a.RT;
-  // blocks of a cluster: as many as stay resident together, while each warp
-  // keeps at least two blocks of 16 keys of the longest request allowed
-  const int64_t slots = static_cast<int64_t>(device_sm_count()) * own_blocks(D, NT);
-  int cl = 1;
-  while (cl < kMaxCluster && 2 * base * cl <= slots && p.S >= 2 * 16 * kOwnWarps * 2 * cl) cl *= 2;
-  a.cluster = cl;
-  a.longest_first = p.S > 0 && base * cl > slots && p.B > 1 && p.B <= kMaxSorted;
-  const int64_t blocks = base * cl;
+  const int64_t base = p.B * p.Hkv * a.RT, blocks = base * pl.chunks;
+  const int64_t slots = static_cast<int64_t>(device_sm_count()) * OwnCfg<D, 1, true>::BLOCKS;
+  a.len_scale = 4194304.f / static_cast<float>(p.S + 1);
+  a.longest_first = p.S > 0 && pl.chunks == 1 && base > slots && p.B > 1 && p.B <= kMaxSorted;
   if (blocks > 0x7fffffffLL) return FA_ERR_SHAPE;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-  cfg.blockDim = dim3(kOwnThreads);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  cfg.attrs = attr;
-  cfg.numAttrs = 0;
-  if (cl > 1) {
-    cudaLaunchAttribute& at = attr[cfg.numAttrs++];
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = static_cast<unsigned>(cl);
-    at.val.clusterDim.y = 1;
-    at.val.clusterDim.z = 1;
+  // The own rows need nothing of the prefix kernel until their sums are joined,
+  // where every block waits for it (griddepcontrol.wait): the blocks start on
+  // SMs that the prefix kernel has left.  Without that kernel before it the
+  // launch is an ordinary one.
+  const auto launch = [&](auto kern, int64_t grid, int smem, bool overlap) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(kOwnThreads);
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = overlap ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, a) == cudaSuccess && cudaGetLastError() == cudaSuccess;
+  };
+  bool ok;
+#define FA_OWN(NT, DEEP)                                                                  \
+  do {                                                                                    \
+    FA_CONFIGURE((own_kernel<T, D, NT, DEEP>), (OwnCfg<D, NT, DEEP>::SMEM));              \
+    ok = launch(own_kernel<T, D, NT, DEEP>, blocks, OwnCfg<D, NT, DEEP>::SMEM, pl.ns > 0); \
+  } while (0)
+  const bool deep = pl.chunk > kDeepRows || blocks <= slots;
+  if (rows == 8) {
+    if (deep) FA_OWN(1, true);
+    else FA_OWN(1, false);
+  } else {
+    if (deep) FA_OWN(2, true);
+    else FA_OWN(2, false);
   }
-  if (pl.ns > 0) {
-    // The own rows need nothing of the prefix kernel until the join, where
-    // every block waits for it (griddepcontrol.wait): its blocks start on SMs
-    // that the prefix kernel has left.  Without that kernel before it the
-    // launch is an ordinary one.
-    cudaLaunchAttribute& at = attr[cfg.numAttrs++];
-    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at.val.programmaticStreamSerializationAllowed = 1;
-  }
-  auto kern = NT == 1 ? own_kernel<T, D, 1> : own_kernel<T, D, 2>;
-  if (cudaLaunchKernelEx(&cfg, kern, a) != cudaSuccess) return FA_ERR_LAUNCH;
-  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+#undef FA_OWN
+  // an ordinary launch: the join reads the sums of both kernels
+  if (ok && pl.chunks > 1) ok = launch(join_kernel<T>, (p.Hkv * R + kOwnWarps - 1) / kOwnWarps, 0, false);
+  return ok ? FA_OK : FA_ERR_LAUNCH;
 }
 
 }  // namespace
 
-PrefixPlan decode_plan(int64_t B, int64_t Hkv, int64_t GN, int64_t D, int64_t P) {
-  return make_plan(B, Hkv, GN, D, P);
+DecodePlan decode_plan(int64_t B, int64_t Hkv, int64_t GN, int64_t D, int64_t P, int64_t S) {
+  DecodePlan pl{};
+  pl.chunks = 1;
+  if (P > 0) plan_prefix(B * GN, Hkv, D, P, &pl);
+  const int rows = own_rows(GN);
+  plan_own(B * Hkv * ((GN + rows - 1) / rows), D, S, &pl);
+  // per range, chunk and query row: D sums and a log-sum-exp
+  const int64_t R = Hkv * B * GN, own = pl.chunks > 1 ? pl.chunks * R * (D + 1) : 0;
+  pl.floats = pl.ns * R * D + (pl.ns * R + 3) / 4 * 4 + own;
+  return pl;
 }
 
 fa_status launch_decode(const DecodeParams& p, cudaStream_t s) {

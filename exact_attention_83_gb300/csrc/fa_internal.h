@@ -261,13 +261,14 @@ struct DecodeParams {
   unsigned int* status;
   uint64_t timeout_ns;
 };
-// How fa_decode cuts the prefix: ns ranges of key tiles (0: no prefix), row
-// groups of 256 (two = 1) or 128 query rows.
-struct PrefixPlan {
-  int ns, two;
-  int64_t groups;
+// How fa_decode cuts its work: ns ranges of the prefix's key tiles (0: no
+// prefix) for row groups of 256 (two = 1) or 128 query rows, and chunks of
+// `chunk` own rows per request; floats: the workspace that takes.
+struct DecodePlan {
+  int ns, two, chunks;
+  int64_t groups, chunk, floats;
 };
-PrefixPlan decode_plan(int64_t B, int64_t Hkv, int64_t GN, int64_t D, int64_t P);
+DecodePlan decode_plan(int64_t B, int64_t Hkv, int64_t GN, int64_t D, int64_t P, int64_t S);
 fa_status launch_decode(const DecodeParams& p, cudaStream_t s);
 
 // Records prof[i] on s when profiling events are set.

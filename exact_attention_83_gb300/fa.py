@@ -654,8 +654,8 @@ def _decode_bytes(sizes) -> int:
 
 
 def decode_workspace_bytes(q, k_prefix, k) -> int:
-    """Bytes of the workspace decode needs for these shapes (0 if invalid, or
-    without a prefix)."""
+    """Bytes of the workspace decode needs for these shapes (0 if none, or if they
+    are invalid)."""
     return _decode_bytes(_decode_sizes(q, k_prefix, k))
 
 
