@@ -594,21 +594,24 @@ def _dense(t: torch.Tensor) -> torch.Tensor:
 class _ApplyRotary(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, q_weight, k_weight, rot):
-        norm = q_weight is not None
-        ctx.rot = rot._replace(q_weight=None, k_weight=None)
-        # without a norm the gradient needs no input
-        ctx.save_for_backward(*((q, k, q_weight, k_weight) if norm else ()))
+        # Positions and frequencies are saved like inputs, so that a change in
+        # place before the backward is an error; without a norm the gradient
+        # needs neither q nor k.
+        norm = (q, k, q_weight, k_weight) if q_weight is not None else ()
+        ctx.save_for_backward(rot.positions, rot.inv_freq, *norm)
+        ctx.rot = rot._replace(positions=None, inv_freq=None, q_weight=None, k_weight=None)
         return _apply_fwd(q, k, rot, None)
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, dqo, dko):
         dqo, dko = _dense(dqo), _dense(dko)
-        if not ctx.saved_tensors:
-            return (*_apply_bwd(None, None, dqo, dko, ctx.rot, None), None, None, None)
-        q, k, qw, kw = ctx.saved_tensors
-        dq, dk, dqw, dkw = _apply_bwd(q, k, dqo, dko, ctx.rot._replace(q_weight=qw, k_weight=kw),
-                                      None)
+        positions, inv_freq, *norm = ctx.saved_tensors
+        rot = ctx.rot._replace(positions=positions, inv_freq=inv_freq)
+        if not norm:
+            return (*_apply_bwd(None, None, dqo, dko, rot, None), None, None, None)
+        q, k, qw, kw = norm
+        dq, dk, dqw, dkw = _apply_bwd(q, k, dqo, dko, rot._replace(q_weight=qw, k_weight=kw), None)
         return dq, dk, dqw.to(qw.dtype), dkw.to(kw.dtype), None
 
 

@@ -268,3 +268,62 @@ def test_own_rows_past_32_bit_offsets():
     o, lse = fa.attention_decode(q, small["kp"], small["vp"], k, v, lens)
     torch.cuda.synchronize()
     check(small, (o[-1:], lse[-1:]))
+
+
+@pytest.mark.parametrize("Hq,Hkv,Nq", [(4, 1, 1), (8, 2, 3), (20, 1, 2)])
+@pytest.mark.parametrize("P", [0, 300])
+def test_chunks_of_long_requests(P, Hq, Hkv, Nq):
+    """Few requests with many rows: chunks that end inside, at and behind a
+    length, lengths of zero and one among them, and lengths out of range."""
+    S = 4096
+    lens = [4096, 0, 1, 512, 513, 1023, 3000]
+    for D, dtype in ((128, "bf16"), (64, "fp16")):
+        t = make(7, Hq, Hkv, Nq, D, P, S, lens, dtype, seed=Nq)
+        assert fa.decode_workspace_bytes(t["q"], t["kp"], t["k"]) > fa.decode_workspace_bytes(
+            t["q"], t["kp"], t["k"][:, :, :64])        # it is cut into chunks
+        check(t, run(t))
+    o, lse = torch.full_like(t["q"], 7.0), torch.full(t["q"].shape[:3], 7.0, device=DEV)
+    ws = torch.full((fa.decode_workspace_bytes(t["q"], t["kp"], t["k"]) // 4,), float("nan"), device=DEV)
+    t["lens"][1], t["lens"][4] = -3, S + 1
+    fa.decode(t["q"], t["kp"], t["vp"], t["k"], t["v"], t["lens"], o, lse, workspace=ws)
+    torch.cuda.synchronize()
+    assert fa.device_status() == 13
+    assert all((x[i] == 7).all() for x in (o, lse) for i in (1, 4))
+    t["lens"][1] = t["lens"][4] = 0
+    check(t, (o, lse), rows=[0, 2, 3, 5, 6])
+
+
+@pytest.mark.parametrize("B", [200, 256, 257, 300])
+def test_more_requests_than_blocks(B):
+    """Requests taken by falling length (up to 256 of them) and in their order
+    (above), with equal lengths and lengths out of range among them."""
+    S = 120
+    lens = [(i * 37) % 121 for i in range(B)]
+    t = make(B, 8, 8, 1, 64, 40, S, lens, "fp16", seed=B)
+    check(t, run(t))
+    t["lens"][3], t["lens"][B - 1] = 2**31 - 1, -2**31
+    o, lse = fa.attention_decode(t["q"], t["kp"], t["vp"], t["k"], t["v"], t["lens"])
+    torch.cuda.synchronize()
+    assert fa.device_status() == 13
+    t["lens"][3] = t["lens"][B - 1] = 0
+    check(t, (o, lse), rows=[i for i in range(B) if i not in (3, B - 1)])
+
+
+def test_captured_graph_of_chunks_and_one_workspace_for_two_graphs_in_turn():
+    t = make(2, 4, 2, 1, 64, 200, 3000, [3000, 10], seed=2, poison=False)
+    args = (t["q"], t["kp"], t["vp"], t["k"], t["v"], t["lens"])
+    ws = torch.empty(fa.decode_workspace_bytes(t["q"], t["kp"], t["k"]) // 4, device=DEV)
+    fa.attention_decode(*args, workspace=ws)
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = fa.attention_decode(*args, workspace=ws)
+        graphs.append((g, out))
+    for step in range(4):
+        t["lens"].copy_(torch.tensor([3000 - 900 * step, 10 + 990 * step], dtype=torch.int32))
+        t["q"].copy_(torch.randn_like(t["q"]))
+        g, out = graphs[step % 2]
+        g.replay()
+        torch.cuda.synchronize()
+        check(t, out)

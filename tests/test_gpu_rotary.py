@@ -354,3 +354,44 @@ def test_attention_applies_the_rotation_first():
     o = fa.attention_varlen(qp, kp, vp, cu, cu, 40, 40, causal=True, rotary=rot)
     q2, k2 = fa.qk_norm_rotary_fwd(qp, kp, qw.detach(), kw.detach(), rot.positions, rot.inv_freq)
     assert torch.equal(o, fa.attention_varlen(q2, k2, vp, cu, cu, 40, 40, causal=True))
+
+
+def test_positions_changed_before_the_backward_are_an_error():
+    """A decode loop that advances its positions in place must not change the
+    gradient of an earlier call in silence."""
+    q = torch.randn(2, 4, 12, 32, device=DEV, requires_grad=True)
+    pos, freq = torch.arange(12, device=DEV), torch.rand(16, device=DEV)
+    a, b = fa.rotary(q, q.detach(), pos, freq)
+    pos += 1
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        a.sum().backward()
+
+
+def test_several_calls_at_once():
+    """Two streams; each call allocates its own workspace."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(4)
+    xs = [(_heads(g, 1, 16, 3000, 128, torch.bfloat16, "packed"), _heads(g, 1, 4, 3000, 128, torch.bfloat16, "packed"))
+          for _ in range(2)]
+    w, freq, pos = torch.rand(128, device=DEV), torch.rand(64, device=DEV), torch.arange(3000, device=DEV)
+    ref = [fa.qk_norm_rotary_bwd(q, k, w, w, q, k, pos, freq) for q, k in xs]
+    torch.cuda.synchronize()
+    got = []
+    for q, k in xs:
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(4):
+                r = fa.qk_norm_rotary_bwd(q, k, w, w, q, k, pos, freq)
+            got.append(r)
+    torch.cuda.synchronize()
+    for a, b in zip(ref, got):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (2, 1), (33, 7), (100, 3)])
+@pytest.mark.parametrize("D", [16, 64, 128])
+def test_head_counts_and_tiles(D, Hq, Hkv, interleaved):
+    """Fewer heads than a warp has rows, heads that leave lanes over, and lengths
+    around every tile size."""
+    for N in (3, 17, 130):
+        _check("bf16", 2, N, Hq, Hkv, D, [8] if D == 16 else [8, D // 2 - 8], interleaved, "bnhd", True, seed=Hq + N)
