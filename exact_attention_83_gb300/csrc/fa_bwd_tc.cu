@@ -74,6 +74,7 @@ struct BwdTcArgs {
   int split;               // dK/dV kernel: CTAs (one cluster) sharing a key tile's query heads
   unsigned int* status;
   uint64_t timeout_ns;
+  PackedOrder order;       // template flags ZR and PFX
 };
 
 // ============================================================================
@@ -155,10 +156,15 @@ __global__ void __launch_bounds__(320, 1)
   const int64_t id = blockIdx.x / split;
   // Grouped order (grouped_tile): the key-tile CTAs in flight belong to a few
   // heads, whose Q and dO tiles stay in L2; low key tiles (most work) first.
-  int64_t bhk, kt;                              // b * Hkv + key/value head, key tile
-  grouped_tile(id, a.BH, a.ntiles, a.hgroup, bhk, kt);
-  const int64_t bseq = bhk / a.g.Hkv;
-  const int32_t hk = static_cast<int32_t>(bhk % a.g.Hkv);
+  int64_t bhk, kt, bseq, hk64;                  // b * Hkv + key/value head, key tile
+  if (ZR && a.order.on) {
+    if (!packed_tile(a.order, a.g.cu_k, a.g.B, a.g.Nk, C::BT, a.g.Hkv, id, false, hk64, bseq, kt)) return;
+  } else {
+    grouped_tile(id, a.BH, a.ntiles, a.hgroup, bhk, kt);
+    bseq = bhk / a.g.Hkv;
+    hk64 = bhk % a.g.Hkv;
+  }
+  const int32_t hk = static_cast<int32_t>(hk64);
   const SeqView sv = seq_view(a.g, bseq);
   if (!sv.ok) {
     if (threadIdx.x == 0) record_status(a.status, FA_ERR_SEQLENS);
@@ -1250,11 +1256,18 @@ __global__ void __launch_bounds__(320, 1)
   const int64_t id = blockIdx.x;
   // Grouped order (grouped_tile): the query-tile CTAs in flight belong to a
   // few heads, whose K and V tiles stay in L2; the longest tiles first.
-  int64_t bh, t;                                // b * Hq + h
-  grouped_tile(id, a.BH, a.ntiles, a.hgroup, bh, t);
-  const int64_t qt = a.causal ? (a.ntiles - 1 - t) : t;
-  const int64_t h = bh % a.g.Hq;
-  const SeqView sv = seq_view(a.g, bh / a.g.Hq);
+  int64_t bh, t, h, bseq, qt;                   // bh = b * Hq + h; query tile
+  if (PFX && a.order.on) {
+    if (!packed_tile(a.order, a.g.cu_q, a.g.B, a.g.Nq, C::BT, a.g.Hq, id, a.causal != 0, h, bseq, qt))
+      return;
+    bh = bseq * a.g.Hq + h;
+  } else {
+    grouped_tile(id, a.BH, a.ntiles, a.hgroup, bh, t);
+    qt = a.causal ? (a.ntiles - 1 - t) : t;
+    h = bh % a.g.Hq;
+    bseq = bh / a.g.Hq;
+  }
+  const SeqView sv = seq_view(a.g, bseq);
   if (!sv.ok) {
     if (threadIdx.x == 0) record_status(a.status, FA_ERR_SEQLENS);
     return;
@@ -1770,8 +1783,9 @@ fa_status launch_dkdv_zr(const BwdParams& p, const Geo& g, const CUtensorMap& mq
   int split = 1;
   while (split < 8 && g.G % (2 * split) == 0 && base * split < 2 * device_sm_count()) split *= 2;
   a.split = split;
-  const int64_t blocks = base * split;
-  if (blocks > 0x7fffffffLL) return FA_ERR_SHAPE;
+  if (base * split > 0x7fffffffLL) return FA_ERR_SHAPE;
+  a.order = g.cu_k ? packed_order(g, g.Hkv, g.rows_k, 128, base, 0, p.D) : PackedOrder{};
+  const int64_t blocks = (a.order.on ? g.Hkv * a.order.bound : base) * split;
   auto kern = bwd_dkdv_tc_kernel<T, D, kDropNone, true>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, DkdvCfg<D>::SMEM) !=
       cudaSuccess)
@@ -1838,8 +1852,10 @@ fa_status run_bwd_prefix(const BwdParams& p, cudaStream_t stream) {
   a.split = 1;
   a.BH = g.B * g.Hq; a.ntiles = (g.Nq + 127) / 128;
   a.hgroup = head_group(a.BH, 2 * (g.Nk + p.pfx.P) * p.D * 2);
-  const int64_t blocks = a.BH * a.ntiles;
+  int64_t blocks = a.BH * a.ntiles;
   if (blocks > 0x7fffffffLL) return FA_ERR_SHAPE;
+  a.order = packed_order(g, g.Hq, g.rows_q, 128, blocks, p.pfx.P, p.D);
+  if (a.order.on) blocks = g.Hq * a.order.bound;
   a.out0 = p.dq; a.out1 = nullptr;
   for (int i = 0; i < 4; ++i) { a.s0[i] = p.sdq[i]; a.s1[i] = 0; }
   auto kern = bwd_dq_tc_kernel<T, D, kDropNone, true>;

@@ -99,6 +99,7 @@ struct FwdTcArgs {
   unsigned int* status;
   uint64_t timeout_ns;
   int withhold_arrival;    // test-only: CTA 0 skips the first S-ready arrival of tile 0
+  PackedOrder order;       // template flag PFX
 };
 
 template <typename T, int D, int DROP, bool PFX>
@@ -128,11 +129,18 @@ __global__ void __launch_bounds__(320, 1)
   const int64_t id = blockIdx.x;
   // Grouped order (grouped_tile): the CTAs in flight belong to a few heads,
   // whose K and V tiles stay in L2; the longest query-tile pairs first.
-  int64_t bh, t;                                // b * Hq + h
-  grouped_tile(id, a.BH, a.npairs, a.hgroup, bh, t);
-  const int64_t pr = a.causal ? (a.npairs - 1 - t) : t;
-  const int64_t h = bh % a.g.Hq;
-  const SeqView sv = seq_view(a.g, bh / a.g.Hq);
+  int64_t bh, t, h, bseq, pr;                   // bh = b * Hq + h; query-tile pair
+  if (PFX && a.order.on) {
+    if (!packed_tile(a.order, a.g.cu_q, a.g.B, a.g.Nq, 2 * C::BM, a.g.Hq, id, a.causal != 0, h, bseq, pr))
+      return;
+    bh = bseq * a.g.Hq + h;
+  } else {
+    grouped_tile(id, a.BH, a.npairs, a.hgroup, bh, t);
+    pr = a.causal ? (a.npairs - 1 - t) : t;
+    h = bh % a.g.Hq;
+    bseq = bh / a.g.Hq;
+  }
+  const SeqView sv = seq_view(a.g, bseq);
   if (!sv.ok) {
     if (threadIdx.x == 0) record_status(a.status, FA_ERR_SEQLENS);
     return;
@@ -575,11 +583,18 @@ __global__ void __launch_bounds__(192, 2)
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t id = blockIdx.x;
-  int64_t bh, t;                                // b * Hq + h (grouped order, as above)
-  grouped_tile(id, a.BH, a.npairs, a.hgroup, bh, t);
-  const int64_t qt = a.causal ? (a.npairs - 1 - t) : t;   // query tile
-  const int64_t h = bh % a.g.Hq;
-  const SeqView sv = seq_view(a.g, bh / a.g.Hq);
+  int64_t bh, t, h, bseq, qt;                   // bh = b * Hq + h; query tile
+  if (PFX && a.order.on) {
+    if (!packed_tile(a.order, a.g.cu_q, a.g.B, a.g.Nq, C::BM, a.g.Hq, id, a.causal != 0, h, bseq, qt))
+      return;
+    bh = bseq * a.g.Hq + h;
+  } else {
+    grouped_tile(id, a.BH, a.npairs, a.hgroup, bh, t);    // grouped order, as above
+    qt = a.causal ? (a.npairs - 1 - t) : t;
+    h = bh % a.g.Hq;
+    bseq = bh / a.g.Hq;
+  }
+  const SeqView sv = seq_view(a.g, bseq);
   if (!sv.ok) {
     if (threadIdx.x == 0) record_status(a.status, FA_ERR_SEQLENS);
     return;
@@ -957,13 +972,17 @@ fa_status run_fwd_tc(const FwdParams& p, cudaStream_t stream) {
     px.tiles = static_cast<int>((p.pfx.P + 127) / 128);
     px.lim_last = static_cast<int>((p.pfx.P + 127) % 128);
   }
-  const int64_t blocks = a.BH * a.npairs;
+  int64_t blocks = a.BH * a.npairs;
   if (blocks > 0x7fffffffLL) return FA_ERR_SHAPE;
   if constexpr (D == 64) {
     // one query tile per CTA (npairs counts query tiles here), two CTAs per SM
     a.npairs = (g.Nq + 127) / 128;
-    const int64_t blocks1 = a.BH * a.npairs;
+    int64_t blocks1 = a.BH * a.npairs;
     if (blocks1 > 0x7fffffffLL) return FA_ERR_SHAPE;
+    if constexpr (PFX) {
+      a.order = packed_order(g, g.Hq, g.rows_q, 128, blocks1, p.pfx.P, p.D);
+      if (a.order.on) blocks1 = g.Hq * a.order.bound;
+    }
     auto kern = fwd_tc_1t_kernel<T, DROP, PFX>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Fwd1Cfg::SMEM) !=
         cudaSuccess)
@@ -971,6 +990,10 @@ fa_status run_fwd_tc(const FwdParams& p, cudaStream_t stream) {
     kern<<<dim3(static_cast<unsigned>(blocks1)), dim3(Fwd1Cfg::THREADS), Fwd1Cfg::SMEM, stream>>>(
         mq, mk, mv, a, px);
   } else {
+    if constexpr (PFX) {
+      a.order = packed_order(g, g.Hq, g.rows_q, 256, blocks, p.pfx.P, p.D);
+      if (a.order.on) blocks = g.Hq * a.order.bound;
+    }
     auto kern = fwd_tc_kernel<T, D, DROP, PFX>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
         cudaSuccess)

@@ -117,6 +117,14 @@ inline Geo prefix_geo(const Geo& g, int64_t P) {
   return r;
 }
 
+// Sequences up to which the packed block order (PackedOrder) is used: every
+// block sums up to that many lengths, 128 to a round of loads.  Sequences of 1 to
+// 100 rows and one of 385, 16 heads, 2048 prefix keys, forward in us with the
+// order / without: D = 64 512 sequences 691 / 1010, 1024 1522 / 2019, 2048 3684 /
+// 4016, 4096 10494 / 8018; D = 128 (one block per SM, nothing beside the scan) 256
+// 758 / 765, 512 1533 / 1490, 1024 3232 / 2965.
+constexpr int64_t kMaxPackedOrder = 512;
+
 #ifdef __CUDACC__
 // One sequence as a kernel sees it: batch coordinate of the tensors, first
 // query / key row, lengths.  ok is false when packed offsets are inconsistent

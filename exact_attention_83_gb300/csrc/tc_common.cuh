@@ -333,6 +333,83 @@ struct PrefixMaps<true> {
   int lim_last;    // last valid key of the last one
 };
 
+// Block order without empty blocks for packed sequences of unequal lengths.  A
+// grid sized by the longest sequence leaves blocks past every shorter one, and a
+// block of these kernels holds its SM's shared memory for some microseconds even
+// to find that out (24 sequences of 1 to 257 rows behind 2048 keys, 592 blocks of
+// 1152 with work: forward 68 us, 51 in this order; 128 sequences of up to 100 rows
+// and one of 1025, 16 heads: 353 -> 177 us and 754 -> 554 backward at D = 64, 443 ->
+// 390 and 883 -> 672 at D = 128).  Here the blocks are numbered over the tiles that
+// exist:
+// `bound` >= their number per head (rows / tile + sequences), heads in groups of
+// `hg` that share keys in L2, and the tiles past the last one at each group's
+// end.  Every warp finds the block's sequence by summing the sequences' tiles.
+struct PackedOrder {
+  int on, bound, hg;
+};
+// The order for `H` heads over `total` packed rows in tiles of `rows`, on when it
+// takes fewer blocks than the `blocks` of a grid over the longest sequence; the
+// heads of a group share the prefix's and a sequence's keys.
+inline PackedOrder packed_order(const Geo& g, int64_t H, int64_t total, int rows, int64_t blocks, int64_t P,
+                                int64_t D) {
+  PackedOrder o{};
+  const int64_t bound = total / rows + g.B;
+  if (g.B > kMaxPackedOrder || bound * H >= blocks) return o;
+  o.on = 1;
+  o.bound = static_cast<int>(bound);
+  const int64_t per = H / g.Hkv;               // heads that read one key/value head
+  o.hg = static_cast<int>(per * head_group(g.Hkv, 4 * (P + g.Nk) * D));
+  return o;
+}
+// Block `id` -> head h of H, sequence b, tile t of `rows` rows (the last tile
+// first when `last_first`); false: past the last tile.  An empty sequence and one
+// with inconsistent offsets count one tile, whose block reports what is wrong
+// with the sequence; the first bad one lies below `bound`, since those before it
+// are disjoint.  Every lane of the warp must call it.
+__device__ __forceinline__ bool packed_tile(const PackedOrder& po, const int32_t* cu, int64_t B,
+                                            int64_t most, int rows, int64_t H, int64_t id,
+                                            bool last_first, int64_t& h, int64_t& b, int64_t& t) {
+  const uint32_t i = static_cast<uint32_t>(id), hg = static_cast<uint32_t>(po.hg);
+  const uint32_t per = hg * static_cast<uint32_t>(po.bound), grp = i / per, rem = i - grp * per;
+  const uint32_t gh = static_cast<uint32_t>(H) - grp * hg < hg ? static_cast<uint32_t>(H) - grp * hg : hg;
+  const int ft = static_cast<int>(rem / gh);           // tile, counted over the sequences
+  h = grp * hg + rem % gh;
+  const int lane = threadIdx.x & 31;
+  int base = 0;
+  for (int64_t b0 = 0; b0 < B; b0 += 128) {
+    int n[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {                       // 128 sequences' loads at once
+      const int64_t s = b0 + 32 * c + lane;
+      n[c] = 0;
+      if (s < B) {
+        const int64_t len = static_cast<int64_t>(__ldg(cu + s + 1)) - __ldg(cu + s);
+        n[c] = len < 1 || len > most ? 1 : static_cast<int>((len + rows - 1) / rows);
+      }
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      int incl = n[c];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+      }
+      const uint32_t past = __ballot_sync(0xffffffffu, base + incl > ft);
+      if (past != 0u) {
+        const int src = __ffs(past) - 1;
+        const int first = base + __shfl_sync(0xffffffffu, incl - n[c], src);
+        const int tiles = __shfl_sync(0xffffffffu, n[c], src);
+        b = b0 + 32 * c + src;
+        t = last_first ? tiles - 1 - (ft - first) : ft - first;
+        return true;
+      }
+      base += __shfl_sync(0xffffffffu, incl, 31);
+    }
+  }
+  return false;
+}
+
 // Zeroes row `row` of a 128-byte-swizzled tile of `chunks` chunks
 // (64-column chunks of 128 rows x 128 bytes): the rows of an operand tile past
 // the sequence, whose weights are 0, may hold anything, and 0 times an

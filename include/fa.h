@@ -350,8 +350,9 @@ FA_API fa_status fa_dropout_mask(const fa_problem* prob, uint8_t* mask, size_t b
  * the schedule (no atomics).  Rows that belong to no sequence (before
  * cu_seqlens[0], past cu_seqlens[B]) are neither used nor written, whatever they
  * hold.  A sequence whose offsets break
- * fa_problem's rules is skipped and reported as there (FA_ERR_SEQLENS); the
- * gradients of the prefix are then not defined.
+ * fa_problem's rules is skipped and reported as there (FA_ERR_SEQLENS); sequences
+ * behind it may be skipped too, and the gradients of the prefix are then not
+ * defined.
  *
  * Errors as for fa_fwd_ex / fa_bwd_ex, plus FA_ERR_SHAPE for P < 0 or sequences
  * that are not packed, FA_ERR_ARG for dropout_p > 0.

@@ -207,6 +207,41 @@ def test_many_sequences_and_a_long_prefix():
     both(make((1500, 700), (1500, 700), 2, 1, 128, 3000, seed=6))
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("fp16", 64), ("bf16", 32)])
+def test_one_long_sequence_among_short_ones(dtype, D, causal):
+    """Far fewer tiles than sequences x the longest one's; some are empty."""
+    lens = [(i * 37) % 7 for i in range(140)]
+    lens[0], lens[129], lens[139] = 0, 700, 0
+    both(make(lens, lens, 4, 2, D, 70, dtype, seed=17, lead=2, tail=3), causal)
+
+
+@pytest.mark.parametrize("n", [511, 512, 513])
+def test_sequence_counts_around_the_limit_of_the_packed_order(n):
+    lens = [1 + i % 3 for i in range(n)]
+    lens[n // 2] = 400
+    both(make(lens, lens, 2, 1, 64, 40, "bf16", seed=18))
+
+
+def test_long_sequences_of_unequal_length_and_many_heads():
+    lens = (900, 3, 128, 0, 257, 512)
+    both(make(lens, lens, 12, 6, 128, 200, "bf16", seed=19))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_bad_keys_of_an_empty_sequence_are_reported(D):
+    """Sequences before the bad one keep their rows."""
+    lens = [5, 300, 0, 4, 4, 4, 4, 4, 4]
+    t = make(lens, lens, 2, 2, D, 30, "bf16", seed=20)
+    o = run(t, True, train=False)["o"]
+    bad = t["ck"].clone()
+    bad[3] = 100000
+    got, _ = fa.attention_prefix_fwd(t["q"], t["k"], t["v"], t["kp"], t["vp"], t["cq"], bad, t["mq"], t["mk"], True)
+    torch.cuda.synchronize()
+    assert fa.device_status() == 13 and fa.device_status() == 0
+    assert torch.equal(got[:305], o[:305])
+
+
 def test_scale_strides_and_slices():
     """Rows of a fused projection [rows, 3, H, D] and a prefix that is a slice of
     a longer cache."""
