@@ -371,7 +371,9 @@ __global__ void __launch_bounds__(320, 1)
           m = m_new;
         }
       }
-      const uint64_t cc = f32x2(c, c), nm = f32x2(-m, -m);
+      // no finite score yet: exponents against 0, so that -inf stays a weight of 0
+      const float ms = m == -INFINITY ? 0.f : m;
+      const uint64_t cc = f32x2(c, c), nm = f32x2(-ms, -ms);
       uint64_t acc = f32x2(0.f, 0.f);
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
@@ -456,7 +458,7 @@ __global__ void __launch_bounds__(320, 1)
         m = mm;
         other = reinterpret_cast<const float*>(sRing) + (128 + r) * D;
       }
-      const float inv = 1.f / l;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
       stage(w0 * inv, w1 * inv, other);
       if (r < nrows[g])
         a.part_l[prow0 + row0 + (two ? 128 * g : 0) + r] = m + log2f(l);
@@ -917,7 +919,6 @@ template <typename T>
 __global__ void __launch_bounds__(kOwnThreads) join_kernel(const __grid_constant__ OwnArgs a) {
   constexpr int PIECES = kMaxRanges + kMaxChunks;
   __shared__ float sW[kOwnWarps][PIECES];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * kOwnWarps + warp;   // of Hkv * R
   if (row >= static_cast<int64_t>(a.Hkv) * a.R) return;
@@ -925,7 +926,7 @@ __global__ void __launch_bounds__(kOwnThreads) join_kernel(const __grid_constant
   const int b = r / a.GN, gr = r - b * a.GN, hg = gr / a.Nq, tok = gr - hg * a.Nq;
   const int len = __ldg(a.lens + b);
   if (len < 0 || len > a.S) return;          // reported by own_kernel
-  const int nc = (len + a.chunk - 1) / a.chunk, n = a.ns + nc;
+  const int nc = len / a.chunk + (len % a.chunk != 0), n = a.ns + nc;
   auto piece_l = [&](int i) {
     return i < a.ns ? a.part_l[(static_cast<int64_t>(hk) * a.ns + i) * a.R + r]
                     : a.own_l[(static_cast<int64_t>(hk) * a.chunks + i - a.ns) * a.R + r];

@@ -177,6 +177,19 @@ def test_infinite_values_in_masked_places():
     assert torch.equal(o[:, :, :2], o2[:, :, :2]) and torch.equal(lse[:, :, :2], lse2[:, :, :2])
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("B,Hq", [(2, 2), (140, 2)])
+def test_prefix_keys_with_scores_of_minus_infinity(B, Hq, D):
+    """Keys that hold -inf where every query is positive weigh nothing: whole
+    tiles and ranges of the prefix, its whole, and own rows too."""
+    for dead in (300, 900):
+        t = make(B, Hq, 1, 1, D, 900, 40, [1 + i % 40 for i in range(B)], seed=dead + B)
+        t["q"][..., 3] = t["q"][..., 3].abs() + 0.5
+        t["kp"][:, :dead, 3] = -math.inf
+        t["k"][:, :, 20:30, 3] = -math.inf
+        check(t, run(t))
+
+
 def test_bad_lengths_are_reported_and_skipped():
     t = make(4, 4, 2, 1, 64, 100, 20, [20, 21, -1, 7], seed=1, poison=False)
     o = torch.full_like(t["q"], 7.0)
