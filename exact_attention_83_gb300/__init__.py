@@ -5,9 +5,9 @@ include/fa.h); `fa` is its thin Python binding.
 """
 
 from .fa import (FAError, Rotary, attention, attention_bwd, attention_decode, attention_fwd,
-                 attention_varlen_prefix, bwd, bwd_preprocess, device_status, fwd, load_library, qk_norm_rotary, rotary, set_path,
-                 set_wait_timeout_ns)
+                 attention_varlen_prefix, bwd, bwd_preprocess, device_status, fwd, load_library,
+                 qk_norm_rotary, rotary, set_path, set_wait_timeout_ns)
 
 __all__ = ["FAError", "Rotary", "attention", "attention_bwd", "attention_decode", "attention_fwd",
-           "attention_varlen_prefix", "bwd", "bwd_preprocess", "device_status", "fwd", "load_library", "qk_norm_rotary",
-           "rotary", "set_path", "set_wait_timeout_ns"]
+           "attention_varlen_prefix", "bwd", "bwd_preprocess", "device_status", "fwd",
+           "load_library", "qk_norm_rotary", "rotary", "set_path", "set_wait_timeout_ns"]

@@ -221,7 +221,7 @@ __device__ __forceinline__ void stage_keys(const KeyWalk<T>& w, int t, float* ks
   const bool pre = t < w.np;
   stage<T, D, BC, NT>(ks, pre ? w.kp : w.k, pre ? w.skp : w.sk, w.first(t), w.keys(t));
   stage<T, D, BC, NT>(vs, pre ? w.vp : w.v, pre ? w.svp : w.sv, w.first(t), w.keys(t));
-  }
+}
 
 // Block id -> (flat head of the query side, query tile), longest tiles first
 // under a causal mask; false when the tile lies past its sequence.
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(16 * TY) fwd_prefix_ffma_kernel(const __grid_c
   const int64_t hk = h / a.g.G;
   const KeyWalk<T> w = key_walk<T>(a, s, hk, a.causal ? min(s.nk, q0 + BR) : s.nk);
   stage<T, D, BR, NT>(Qs, static_cast<const T*>(a.q) + s.b * a.sq[0] + h * a.sq[1] + s.q0 * a.sq[2], a.sq[2], q0,
-                  s.nq);
+                      s.nq);
   if (rank < w.n) stage_keys<T, D, NT>(w, rank, KV, KV + BC * LD);
   const float c = a.scale * kLog2e;
   float m[TM], l[TM], acc[TM][D / 16];
@@ -395,8 +395,8 @@ __device__ __forceinline__ void dkdv_block(const Args& a, const Geo& g, bool pre
     float* Qs = QG + buf * 2 * BC * LD;
     stage<T, D, BC, NT>(Qs, static_cast<const T*>(a.q) + h * a.sq[1] + s.q0 * a.sq[2], a.sq[2], q0, s.nq);
     stage<T, D, BC, NT>(Qs + BC * LD, static_cast<const T*>(a.dout) + h * a.sdo[1] + s.q0 * a.sdo[2], a.sdo[2], q0,
-                    s.nq);
-        static_assert(NT >= BC, "one L and Delta per thread");
+                        s.nq);
+    static_assert(NT >= BC, "one L and Delta per thread");
     if (threadIdx.x < BC) {
       const int64_t row = q0 + threadIdx.x, li = lse_index(g, s, h, row);
       LDl[buf * 2 * BC + threadIdx.x] = row < s.nq ? a.lse_in[li] * kLog2e : 0.f;

@@ -617,7 +617,9 @@ class _ApplyRotary(torch.autograd.Function):
 
 def apply_rotary(q, k, rot: Rotary):
     """(q', k') of a Rotary, with autograd for q, k and the norm's weights.
-    Second-order gradients are refused."""
+    Second-order gradients are refused, and so are frequencies that want one."""
+    if rot.inv_freq.requires_grad and torch.is_grad_enabled():
+        raise ValueError("inv_freq takes no gradient")
     return _ApplyRotary.apply(_dense(q), _dense(k), rot.q_weight, rot.k_weight, rot)
 
 

@@ -132,6 +132,8 @@ def test_python_refusals():
         fa.rotary_fwd(x, x, torch.arange(8), torch.ones(32))
     with pytest.raises(TypeError):
         fa.attention_decode(x, x[0], x[0], x, x, torch.zeros(2, dtype=torch.int32))
+    with pytest.raises(ValueError, match="no gradient"):
+        fa.rotary(x, x, torch.arange(8), torch.ones(32, requires_grad=True))
 
 
 def test_packed_structs_have_the_c_layout():
