@@ -18,10 +18,10 @@
 //    range leaves partial sums in the workspace (fp32).
 //  * own_kernel: a request's own rows are read by its G * Nq query rows alone.
 //    That is bound by HBM at any rate the matrix units run, so its warps stream K
-//    and V through rings in shared memory into m16n8k16 products.  Requests with
-//    many rows are cut into chunks; with one chunk per request (the usual case)
-//    the kernel also joins all partial sums and writes o and L, otherwise
-//    join_kernel does.
+//    and V through rings in shared memory into m16n8k16 products.  It also joins
+//    all partial sums and writes o and L, unless requests with many rows are cut
+//    into chunks or the own rows run beside a long prefix (plan_prefix): then
+//    its blocks wait for nothing and join_kernel joins.
 //
 // Rows past a request's length are never read: what they hold does not matter.
 
@@ -520,13 +520,13 @@ __global__ void __launch_bounds__(320, 1)
 // round; movmatrix turns them.  16-byte unit u of row r lies at unit
 // u ^ 4 (r mod 2) of its row for K and u ^ 2 (r / 2 mod 4) for V, which spreads
 // the eight reads of a quarter of a warp over all banks.
-// With one chunk per request the block also joins its sums with the prefix's and
-// writes o and L; otherwise it leaves its sums for join_kernel.
+// The block joins its sums with the prefix's and writes o and L, or (apart) leaves
+// its sums for join_kernel.
 constexpr int kOwnThreads = 128;
 constexpr int kOwnWarps = kOwnThreads / 32;
 constexpr int kMaxRanges = 64;            // ranges of the prefix
 constexpr int kMaxChunks = 64;            // chunks of a request's own rows
-constexpr int kMaxSorted = 256;           // requests that a block ranks by length
+constexpr int kMaxSorted = 128;           // requests that a block ranks by length
 constexpr int kDeepRows = 1024;           // rows per block above which deep rings pay (OwnCfg)
 
 struct OwnArgs {
@@ -542,10 +542,11 @@ struct OwnArgs {
   int longest_first;                 // blocks take the requests by falling length
   float len_scale;                   // 2^22 / (S + 1)
   int chunks, chunk;                 // chunks of `chunk` rows (a multiple of 64) per request
+  int apart;                         // sums are left for join_kernel
   int ns, R;                         // prefix partial sums (ns = 0: none)
   const float* part_o;               // [Hkv][ns][R][dreal]
   const float* part_l;               // [Hkv][ns][R]
-  float* own_o;                      // [Hkv][chunks][R][dreal]; chunks > 1
+  float* own_o;                      // [Hkv][chunks][R][dreal]; apart
   float* own_l;                      // [Hkv][chunks][R]
   unsigned int* status;
 };
@@ -629,10 +630,9 @@ __global__ void __launch_bounds__(kOwnThreads, (OwnCfg<D, NT, DEEP>::BLOCKS))
   int b = id / a.Hkv;
   if (a.longest_first) {
     // Blocks start in the order of their index, and a long request that starts
-    // last leaves the GPU idle around it (a fifth of the time at 128 requests of
-    // 1 to 1024 rows).  So block b takes the request of rank b by falling
-    // length, which the threads find by counting.  One key holds a length (22
-    // bits of it suffice) and, so that no two are alike, the request.
+    // last leaves the GPU idle around it.  So block b takes the request of rank b
+    // by falling length, which the threads find by counting.  One key holds a
+    // length (22 bits of it suffice) and, so that no two are alike, the request.
     __shared__ __align__(16) int sKey[kMaxSorted];
     __shared__ int sB;
     auto key_of = [&](int i) {
@@ -640,10 +640,11 @@ __global__ void __launch_bounds__(kOwnThreads, (OwnCfg<D, NT, DEEP>::BLOCKS))
       const float f = static_cast<float>(n < 0 ? 0 : n) * a.len_scale;
       return static_cast<int>(f < 4194303.f ? f : 4194303.f) * kMaxSorted + (kMaxSorted - 1 - i);
     };
-    for (int i = threadIdx.x; i < kMaxSorted; i += kOwnThreads) sKey[i] = i < a.B ? key_of(i) : -1;
+    static_assert(kMaxSorted == kOwnThreads, "one request per thread");
+    const int i = static_cast<int>(threadIdx.x), mine = i < a.B ? key_of(i) : -1;
+    sKey[i] = mine;
     __syncthreads();
-    for (int i = threadIdx.x; i < a.B; i += kOwnThreads) {
-      const int mine = sKey[i];
+    if (i < a.B) {
       int before = 0;
 #pragma unroll 8
       for (int j = 0; j < a.B; j += 4) {
@@ -659,8 +660,12 @@ __global__ void __launch_bounds__(kOwnThreads, (OwnCfg<D, NT, DEEP>::BLOCKS))
   const bool bad = len < 0 || len > a.S;
   if (bad && threadIdx.x == 0) record_status(a.status, FA_ERR_SEQLENS);
   const int key_from = ck * a.chunk;
-  if (bad || (a.chunks > 1 && key_from >= len)) {      // nothing to leave: join_kernel knows the length
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+  // Where join_kernel follows, only the last block waits for the prefix kernel, so
+  // that the join finds both kernels' sums; the others leave as they end.
+  const bool waits = !a.apart || blockIdx.x == gridDim.x - 1;
+  if (a.apart) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (bad || (a.apart && key_from >= len)) {           // nothing to leave: join_kernel knows the length
+    if (waits) asm volatile("griddepcontrol.wait;" ::: "memory");
     return;
   }
   const int key_to = len - key_from < a.chunk ? len : key_from + a.chunk;
@@ -833,12 +838,12 @@ __global__ void __launch_bounds__(kOwnThreads, (OwnCfg<D, NT, DEEP>::BLOCKS))
       }
     }
   __syncthreads();
-  // the prefix's partial sums are complete and visible from here on
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  // the prefix's partial sums are complete and visible from here on (unless apart)
+  if (waits) asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  // Per row, the weights of the four warps' sums and, when this is the only
-  // chunk, of the prefix's; warp w takes rows w, w + 4, ...
-  const int ns = a.chunks == 1 ? a.ns : 0;
+  // Per row, the weights of the four warps' sums and, without a join to follow, of
+  // the prefix's; warp w takes rows w, w + 4, ...
+  const int ns = a.apart ? 0 : a.ns;
   const int64_t prow = static_cast<int64_t>(b) * a.GN + r0;    // row within the head's R rows
   const float* pl = a.part_l + static_cast<int64_t>(hk) * a.ns * a.R + prow;
   const int64_t orow = (static_cast<int64_t>(hk) * a.chunks + ck) * a.R + prow;
@@ -867,7 +872,7 @@ __global__ void __launch_bounds__(kOwnThreads, (OwnCfg<D, NT, DEEP>::BLOCKS))
     for (int i = 0; i < kMaxRanges / 32; ++i)
       if (lane + 32 * i < ns) sP[row][lane + 32 * i] = ex2(pre[i] - Lw);
     if (lane == 0) {
-      if (a.chunks > 1) {
+      if (a.apart) {
         a.own_l[orow + row] = L2;
       } else {
         const int gr = r0 + row, hg = gr / a.Nq, tok = gr - hg * a.Nq;
@@ -898,7 +903,7 @@ __global__ void __launch_bounds__(kOwnThreads, (OwnCfg<D, NT, DEEP>::BLOCKS))
 #pragma unroll
     for (int w = 0; w < kOwnWarps; ++w)
       add(sW[row][w], *reinterpret_cast<const float4*>(own_smem + w * C::RING + (row * D + 4 * u4) * 4));
-    if (a.chunks > 1) {
+    if (a.apart) {
       *reinterpret_cast<float4*>(a.own_o + (orow + row) * a.dreal + 4 * u4) = acc;
     } else {
       const int gr = r0 + row, hg = gr / a.Nq, tok = gr - hg * a.Nq;
@@ -910,7 +915,7 @@ __global__ void __launch_bounds__(kOwnThreads, (OwnCfg<D, NT, DEEP>::BLOCKS))
 }
 
 // ============================================================================
-// The join of several chunks
+// The join
 // ============================================================================
 // One warp per output row: the log-sum-exps of all its pieces (prefix ranges,
 // then the chunks that the request's length reaches) give their weights, then
@@ -919,6 +924,7 @@ template <typename T>
 __global__ void __launch_bounds__(kOwnThreads) join_kernel(const __grid_constant__ OwnArgs a) {
   constexpr int PIECES = kMaxRanges + kMaxChunks;
   __shared__ float sW[kOwnWarps][PIECES];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * kOwnWarps + warp;   // of Hkv * R
   if (row >= static_cast<int64_t>(a.Hkv) * a.R) return;
@@ -980,30 +986,6 @@ __global__ void __launch_bounds__(kOwnThreads) join_kernel(const __grid_constant
 // workspace's size must not depend on a device.
 constexpr int kPlanSMs = 152;
 
-// How the prefix is cut.  A block costs a start and an end plus a time per key
-// tile; the ranges' partial sums cost their way through the L2 cache in
-// proportion to their number.  The cheapest number of ranges by that estimate
-// (microseconds; a trace of the blocks gave 10 to 12 beside their tiles).
-void plan_prefix(int64_t R, int64_t Hkv, int64_t D, int64_t P, DecodePlan* pl) {
-  const int64_t n = (P + 127) / 128;
-  pl->two = R > 128;
-  pl->groups = pl->two ? (R + 255) / 256 : 1;
-  const int64_t base = Hkv * pl->groups;
-  const double per_tile = D > 64 ? 1.45 : 0.8, fixed = 11.0;
-  const double join = static_cast<double>(R) * static_cast<double>(Hkv * D) * 8 / 10e6;  // per range
-  double best = 0;
-  const int64_t most = n < kMaxRanges ? n : kMaxRanges;
-  for (int64_t ns = 1; ns <= most; ++ns) {
-    const double waves = static_cast<double>((base * ns + kPlanSMs - 1) / kPlanSMs);
-    const double t = waves * (fixed + per_tile * static_cast<double>((n + ns - 1) / ns)) +
-                     join * static_cast<double>(ns);
-    if (ns == 1 || t < best) {
-      best = t;
-      pl->ns = static_cast<int>(ns);
-    }
-  }
-}
-
 // How the own rows are cut: into chunks of 512 rows at least, as long as that
 // gives SMs without a block one, since several chunks cost a further kernel (4 us
 // and more).  4 requests of up to 32768 rows, 8 heads: 65 us in chunks, 80 when a
@@ -1015,6 +997,63 @@ void plan_own(int64_t base, int64_t D, int64_t S, DecodePlan* pl) {
   pl->chunk = ((S + c - 1) / c + 63) / 64 * 64;
   if (pl->chunk < 64) pl->chunk = 64;
   pl->chunks = static_cast<int>(S > 0 ? (S + pl->chunk - 1) / pl->chunk : 1);
+  pl->apart = pl->chunks > 1;
+}
+
+// How the prefix is cut, and whether the own rows run beside it.  A block costs
+// a start and an end plus a time per key tile, its products' or that of reading
+// the tiles of all blocks at once; the ranges' partial sums cost their way through
+// the L2 cache in proportion to their number (microseconds; a trace of the blocks
+// gave 10 to 12 beside their tiles).  Either
+//  * the prefix takes all SMs, the own rows follow and join everything, or
+//  * (apart) the prefix takes part of the SMs, and the own rows, which HBM bounds
+//    and not the SMs, run on the others in the meantime; join_kernel follows (8
+//    us with its launch, unless chunks need it anyway).
+// The cheaper by that estimate, with requests half as long as S.  8 heads of 128,
+// cold, in us: 128 requests of up to 1024 rows behind 16384 keys 92 and 81 apart,
+// 64 requests 65 and 54, 128 behind 4096 keys 72 and 69; 32 requests of up to 512
+// rows behind 8192 keys 29 and 38.
+void plan_prefix(int64_t B, int64_t R, int64_t Hkv, int64_t D, int64_t P, int64_t S, DecodePlan* pl) {
+  const int64_t n = (P + 127) / 128;
+  pl->two = R > 128;
+  pl->groups = pl->two ? (R + 255) / 256 : 1;
+  const int64_t base = Hkv * pl->groups;
+  const double products = (D > 64 ? 1.5 : 1.0) * (pl->two ? 1.0 : 0.53), fixed = 11.0, hbm = 6.2e6;
+  const double join = static_cast<double>(R) * static_cast<double>(Hkv * D) * 8 / 10e6;  // per range
+  const double own = static_cast<double>(B * Hkv) * static_cast<double>(S) / 2 * static_cast<double>(4 * D) / hbm;
+  const bool chunked = pl->chunks > 1;
+  double best = 0;
+  const int64_t most = n < kMaxRanges ? n : kMaxRanges;
+  for (int64_t ns = 1; ns <= most; ++ns) {
+    const int64_t blocks = base * ns;
+    const double waves = static_cast<double>((blocks + kPlanSMs - 1) / kPlanSMs);
+    const double once = static_cast<double>(blocks < kPlanSMs ? blocks : kPlanSMs);
+    const double reads = once / static_cast<double>(pl->groups) * static_cast<double>(128 * 4 * D) / hbm;
+    const double tiles = static_cast<double>((n + ns - 1) / ns);
+    const double pre = waves * (fixed + (reads > products ? reads : products) * tiles);
+    const double joins = join * static_cast<double>(ns);
+    double t = pre + own + joins;
+    int apart = chunked;
+    if (S > 0 && blocks < kPlanSMs) {
+      // what the SMs left draw of HBM's rate, each a third more than its share at
+      // most, and what the prefix leaves of it; at D <= 64 blocks of both kernels fit
+      // one SM and slow each other
+      const double mixed = D > 64 ? products : 2 * products, per_tile = reads > mixed ? reads : mixed;
+      const double share = 1.3 * static_cast<double>(kPlanSMs - blocks) / kPlanSMs, rest = 1.0 - reads / per_tile;
+      const double pre_b = fixed + per_tile * tiles;
+      const double left = own - pre_b * (share < rest ? share : rest);
+      const double beside = pre_b + (left > 0 ? left : 0.0) + joins + (chunked ? 0.0 : 8.0);
+      if (chunked || beside < t) {
+        t = beside;
+        apart = 1;
+      }
+    }
+    if (ns == 1 || t < best) {
+      best = t;
+      pl->ns = static_cast<int>(ns);
+      pl->apart = apart;
+    }
+  }
 }
 
 // Query rows of a block of own_kernel: 8, or 16 where a request has more.
@@ -1067,14 +1106,20 @@ fa_status run_decode(const DecodeParams& p, cudaStream_t stream) {
   a.RT = static_cast<int>((GN + rows - 1) / rows);
   a.dreal = static_cast<int>(p.D); a.causal = p.causal;
   a.c = p.scale * kLog2e;
-  a.chunks = pl.chunks; a.chunk = static_cast<int>(pl.chunk);
+  a.chunks = pl.chunks; a.chunk = static_cast<int>(pl.chunk); a.apart = pl.apart;
   a.ns = pl.ns; a.R = static_cast<int>(R);
   a.part_o = part_o; a.part_l = part_l; a.own_o = own_o; a.own_l = own_l;
   a.status = p.status;
   const int64_t base = p.B * p.Hkv * a.RT, blocks = base * pl.chunks;
   const int64_t slots = static_cast<int64_t>(device_sm_count()) * OwnCfg<D, 1, true>::BLOCKS;
   a.len_scale = 4194304.f / static_cast<float>(p.S + 1);
-  a.longest_first = p.S > 0 && pl.chunks == 1 && base > slots && p.B > 1 && p.B <= kMaxSorted;
+  // Ranking costs every round of blocks a start, and gains the end of the last long
+  // request: few rounds of long blocks.  8 heads of 128, ranked / not, in us: 64
+  // requests of up to 2048 rows 47 / 54, 96 of 1024 39 / 44, 128 of 1024 52 / 55, 48 of
+  // 700 25 / 27, 128 of 512 37 / 33, 256 of 1024 111 / 89; 16 heads of 64, 128 of 1024
+  // 56 / 51.
+  a.longest_first = p.B > 1 && p.B <= kMaxSorted && pl.chunks == 1 && base > slots &&
+                    base * (256 * 128) <= slots * p.S * D;
   if (blocks > 0x7fffffffLL) return FA_ERR_SHAPE;
   // The own rows need nothing of the prefix kernel until their sums are joined,
   // where every block waits for it (griddepcontrol.wait): the blocks start on
@@ -1108,8 +1153,7 @@ fa_status run_decode(const DecodeParams& p, cudaStream_t stream) {
     else FA_OWN(2, false);
   }
 #undef FA_OWN
-  // an ordinary launch: the join reads the sums of both kernels
-  if (ok && pl.chunks > 1) ok = launch(join_kernel<T>, (p.Hkv * R + kOwnWarps - 1) / kOwnWarps, 0, false);
+  if (ok && pl.apart) ok = launch(join_kernel<T>, (p.Hkv * R + kOwnWarps - 1) / kOwnWarps, 0, true);
   return ok ? FA_OK : FA_ERR_LAUNCH;
 }
 
@@ -1117,12 +1161,11 @@ fa_status run_decode(const DecodeParams& p, cudaStream_t stream) {
 
 DecodePlan decode_plan(int64_t B, int64_t Hkv, int64_t GN, int64_t D, int64_t P, int64_t S) {
   DecodePlan pl{};
-  pl.chunks = 1;
-  if (P > 0) plan_prefix(B * GN, Hkv, D, P, &pl);
   const int rows = own_rows(GN);
   plan_own(B * Hkv * ((GN + rows - 1) / rows), D, S, &pl);
+  if (P > 0) plan_prefix(B, B * GN, Hkv, D, P, S, &pl);
   // per range, chunk and query row: D sums and a log-sum-exp
-  const int64_t R = Hkv * B * GN, own = pl.chunks > 1 ? pl.chunks * R * (D + 1) : 0;
+  const int64_t R = Hkv * B * GN, own = pl.apart ? pl.chunks * R * (D + 1) : 0;
   pl.floats = pl.ns * R * D + (pl.ns * R + 3) / 4 * 4 + own;
   return pl;
 }

@@ -271,9 +271,10 @@ struct DecodeParams {
 };
 // How fa_decode cuts its work: ns ranges of the prefix's key tiles (0: no
 // prefix) for row groups of 256 (two = 1) or 128 query rows, and chunks of
-// `chunk` own rows per request; floats: the workspace that takes.
+// `chunk` own rows per request; apart: the own rows leave their sums for a join;
+// floats: the workspace that takes.
 struct DecodePlan {
-  int ns, two, chunks;
+  int ns, two, chunks, apart;
   int64_t groups, chunk, floats;
 };
 DecodePlan decode_plan(int64_t B, int64_t Hkv, int64_t GN, int64_t D, int64_t P, int64_t S);

@@ -308,8 +308,8 @@ def test_chunks_of_long_requests(P, Hq, Hkv, Nq):
 
 @pytest.mark.parametrize("B", [200, 256, 257, 300])
 def test_more_requests_than_blocks(B):
-    """Requests taken by falling length (up to 256 of them) and in their order
-    (above), with equal lengths and lengths out of range among them."""
+    """Many more blocks than run at once, with equal lengths and lengths out of
+    range among them."""
     S = 120
     lens = [(i * 37) % 121 for i in range(B)]
     t = make(B, 8, 8, 1, 64, 40, S, lens, "fp16", seed=B)
@@ -320,6 +320,49 @@ def test_more_requests_than_blocks(B):
     assert fa.device_status() == 13
     t["lens"][3] = t["lens"][B - 1] = 0
     check(t, (o, lse), rows=[i for i in range(B) if i not in (3, B - 1)])
+
+
+@pytest.mark.parametrize("B,Hkv,D,S", [(128, 3, 128, 1024), (100, 8, 64, 2100), (127, 4, 128, 1200)])
+@pytest.mark.parametrize("P", [0, 40])
+def test_requests_taken_by_falling_length(B, Hkv, D, S, P):
+    lens = [(i * 37) % 121 for i in range(B)]
+    lens[5], lens[70], lens[B - 1] = S, S - 1, S
+    t = make(B, Hkv, Hkv, 1, D, P, S, lens, "fp16", seed=B)
+    check(t, run(t))
+    t["lens"][3], t["lens"][B - 2] = 2**31 - 1, -2**31
+    o, lse = fa.attention_decode(t["q"], t["kp"], t["vp"], t["k"], t["v"], t["lens"])
+    torch.cuda.synchronize()
+    assert fa.device_status() == 13
+    t["lens"][3] = t["lens"][B - 2] = 0
+    check(t, (o, lse), rows=[i for i in range(B) if i not in (3, B - 2)])
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,D,P,S", [(64, 32, 8, 128, 16384, 1024), (128, 8, 8, 64, 9000, 1200),
+                                            (33, 16, 8, 128, 20000, 2048)])
+def test_own_rows_beside_a_long_prefix(B, Hq, Hkv, D, P, S):
+    """Both kernels at once and a join behind them: requests without own rows, a
+    bad length, and a second call right behind the first in the same workspace."""
+    lens = [(i * 131) % (S + 1) for i in range(B)]
+    lens[B - 1] = 0
+    t = make(B, Hq, Hkv, 1, D, P, S, lens, seed=B, poison=False)
+    args = (t["q"], t["kp"], t["vp"], t["k"], t["v"], t["lens"])
+    ws = torch.full((fa.decode_workspace_bytes(t["q"], t["kp"], t["k"]) // 4,), math.nan, device=DEV)
+    got = fa.attention_decode(*args, workspace=ws)
+    q2 = t["q"].flip(0)
+    again = fa.attention_decode(q2, *args[1:], workspace=ws)
+    third = fa.attention_decode(*args, workspace=ws)
+    torch.cuda.synchronize()
+    assert fa.device_status() == 0
+    assert torch.equal(got[0], third[0]) and torch.equal(got[1], third[1])
+    check(t, got)
+    check(dict(t, q=q2), again)
+    t["lens"][0] = -1
+    o, lse = torch.full_like(got[0], 7.0), torch.full_like(got[1], 7.0)
+    fa.decode(*args, o, lse, workspace=ws)
+    torch.cuda.synchronize()
+    assert fa.device_status() == 13
+    assert (o[0] == 7).all() and (lse[0] == 7).all()
+    assert torch.equal(o[1:], got[0][1:]) and torch.equal(lse[1:], got[1][1:])
 
 
 def test_captured_graph_of_chunks_and_one_workspace_for_two_graphs_in_turn():
