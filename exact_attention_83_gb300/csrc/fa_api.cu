@@ -551,8 +551,35 @@ fa_status fa_bwd_prefix(const fa_problem* prob, int64_t P, const void* q, const 
   p.dkp = dk_prefix; p.dvp = dv_prefix;
   for (int i = 0; i < 4; ++i) { p.sdkp[i] = sdkp4[i]; p.sdvp[i] = sdvp4[i]; }
   p.prof = nullptr;
-  if (use_tc(pb.dtype) && have_bwd_tc(pb.D, pb.dtype)) return launch_bwd_tc(p, stream);
+  if (use_tc(pb.dtype) && have_bwd_tc(pb.D, pb.dtype) && !prefix_ffma_pays(p)) return launch_bwd_tc(p, stream);
   return launch_bwd_prefix_ffma(p, stream);
+}
+
+fa_status fa_bwd_prefix_delta(const fa_problem* prob, int64_t P, const void* q, const int64_t* sq,
+                              const void* k_prefix, const int64_t* skp, const void* v_prefix,
+                              const int64_t* svp, const void* k, const int64_t* sk, const void* v,
+                              const int64_t* sv, const void* o, const int64_t* so, const void* dout,
+                              const int64_t* sdo, const float* lse, float* delta,
+                              cudaStream_t stream) {
+  Problem pb{};
+  BwdParams p{};
+  FA_TRY(check_prefix(prob, P, k_prefix, skp, v_prefix, svp, &pb, &p.pfx));
+  const Geo& g = pb.g;
+  FA_TRY(check_dense(q, sq, 1, g.Hq, g.rows_q, pb.dtype, p.sq));
+  FA_TRY(check_dense(k, sk, 1, g.Hkv, g.rows_k, pb.dtype, p.sk));
+  FA_TRY(check_dense(v, sv, 1, g.Hkv, g.rows_k, pb.dtype, p.sv));
+  int64_t t[4];
+  FA_TRY(check_dense(o, so, 1, g.Hq, g.rows_q, pb.dtype, t));
+  FA_TRY(check_dense(dout, sdo, 1, g.Hq, g.rows_q, pb.dtype, p.sdo));
+  FA_TRY(check_f32_vec(lse));
+  FA_TRY(fa_bwd_preprocess(o, dout, delta, 1, g.Hq, g.rows_q, pb.D, so, sdo, pb.dtype, stream));
+  if (pb.dtype == FA_F32 || P >= kFewKeys) return FA_OK;
+  DeviceInfo* dev = nullptr;
+  FA_TRY(device_setup(&dev));
+  p.q = q; p.k = k; p.v = v; p.dout = dout; p.lse = lse;
+  p.g = g; p.D = pb.D; p.causal = pb.causal; p.scale = pb.scale; p.dtype = pb.dtype;
+  p.status = dev->status;
+  return launch_few_keys_delta(p, delta, stream);
 }
 
 size_t fa_dropout_mask_bytes(const fa_problem* prob) {

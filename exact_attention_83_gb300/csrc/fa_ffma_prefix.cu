@@ -26,6 +26,9 @@
 // gradient 33 us (three launches of 64-row blocks with one operand per read:
 // 65 and 282).  Bound by the instructions of one block's steps, four warps per
 // SM; at large sizes by shared-memory reads, twice the FMAs' time.
+//
+// The gradient of small fp16 / bf16 problems takes these kernels too
+// (prefix_ffma_pays): one launch instead of three, and no rounding of P and dS.
 
 #include "tc_common.cuh"
 
@@ -40,6 +43,7 @@ constexpr int PLD = BC + 4;   // leading dimension of P and dS
 struct Args {
   const void* q; const void* k; const void* v; const void* dout;
   void* o; float* lse; const float* lse_in; const float* delta;
+  float* delta_out;           // few_keys_delta_kernel
   void* dq; void* dk; void* dv; void* dkp; void* dvp;
   Geo g, gp;                  // own keys; all query rows against the prefix
   Prefix pfx;
@@ -551,6 +555,58 @@ __global__ void __launch_bounds__(16 * TY) bwd_prefix_ffma_kernel(const __grid_c
   else dq_block<T, D, TY, TM>(a, id - a.n_pre - a.n_own, rank, sm);
 }
 
+// Delta of rows that see few keys.  Delta = sum_j P_j dP_j is the same number as
+// rowsum(dO o O), but O has been rounded: with n keys that error is about 1 / sqrt(n)
+// of the gradient's own rounding, and more where one key takes most of the weight
+// (fp16, two keys per row: dQ was off by 3.2 times what rounding dQ alone costs,
+// 1.4 with this).  A warp takes a row, a lane a key; above kFewKeys the
+// error does not show and rowsum(dO o O) stays.  Launched for prefixes below kFewKeys
+// only; a block per sequence and head, some microseconds.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) few_keys_delta_kernel(const __grid_constant__ Args a) {
+  constexpr int VEC = 16 / sizeof(T);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t h = blockIdx.x % a.g.Hq, hk = h / a.g.G;
+  const SeqView s = seq_view(a.g, blockIdx.x / a.g.Hq);
+  if (!s.ok) {
+    if (threadIdx.x == 0) record_status(a.status, FA_ERR_SEQLENS);
+    return;
+  }
+  const int64_t P = a.pfx.P;
+  // rows with at most kFewKeys keys: all, or the first under a causal mask
+  const int64_t rows = P + s.nk <= kFewKeys ? s.nq : (a.causal ? min(s.nq, kFewKeys - P) : 0);
+  const bool pre = lane < P;
+  const int64_t key = pre ? lane : lane - P;
+  const T* kr = pre ? static_cast<const T*>(a.pfx.k) + hk * a.pfx.sk[1] + key * a.pfx.sk[2]
+                    : static_cast<const T*>(a.k) + hk * a.sk[1] + (s.k0 + key) * a.sk[2];
+  const T* vr = pre ? static_cast<const T*>(a.pfx.v) + hk * a.pfx.sv[1] + key * a.pfx.sv[2]
+                    : static_cast<const T*>(a.v) + hk * a.sv[1] + (s.k0 + key) * a.sv[2];
+  for (int64_t row = warp; row < rows; row += 8) {
+    const int64_t n = P + (a.causal ? min(row + 1, s.nk) : s.nk);
+    const T* q = static_cast<const T*>(a.q) + h * a.sq[1] + (s.q0 + row) * a.sq[2];
+    const T* g = static_cast<const T*>(a.dout) + h * a.sdo[1] + (s.q0 + row) * a.sdo[2];
+    const int64_t li = lse_index(a.g, s, h, row);
+    float sc = 0.f, dp = 0.f;
+    if (lane < n) {
+#pragma unroll 4
+      for (int d = 0; d < D; d += VEC) {
+        const uint4 w[4] = {__ldg(reinterpret_cast<const uint4*>(q + d)), __ldg(reinterpret_cast<const uint4*>(kr + d)),
+                            __ldg(reinterpret_cast<const uint4*>(g + d)), __ldg(reinterpret_cast<const uint4*>(vr + d))};
+        const T* e = reinterpret_cast<const T*>(w);
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+          sc = fmaf(Elem<T>::to_f32(e[i]), Elem<T>::to_f32(e[VEC + i]), sc);
+          dp = fmaf(Elem<T>::to_f32(e[2 * VEC + i]), Elem<T>::to_f32(e[3 * VEC + i]), dp);
+        }
+      }
+    }
+    float sum = lane < n ? exp2f(fmaf(sc, a.scale * kLog2e, -a.lse_in[li] * kLog2e)) * dp : 0.f;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    if (lane == 0) a.delta_out[li] = sum;
+  }
+}
+
 constexpr int fwd_smem(int D, int BR) { return 4 * ((BR + 4 * BC) * (D + 4) + BR * PLD); }
 constexpr int bwd_smem(int D, int BR) {
   return 4 * ((2 * BR + 4 * BC) * (D + 4) + 2 * BR * PLD + 4 * BC);
@@ -621,6 +677,21 @@ fa_status launch_bwd(Args a, cudaStream_t s) {
   return launch(bwd_prefix_ffma_kernel<T, D, TY, TM>, blocks, 16 * TY, bwd_smem(D, TM * TY), a, s);
 }
 
+template <typename T>
+fa_status launch_few_keys(const Args& a, int64_t D, cudaStream_t s) {
+  const int64_t blocks = a.g.B * a.g.Hq;
+  if (blocks > 0x7fffffffLL) return FA_ERR_SHAPE;
+  const dim3 grid(static_cast<unsigned>(blocks)), threads(256);
+  switch (D) {
+    case 16: few_keys_delta_kernel<T, 16><<<grid, threads, 0, s>>>(a); break;
+    case 32: few_keys_delta_kernel<T, 32><<<grid, threads, 0, s>>>(a); break;
+    case 64: few_keys_delta_kernel<T, 64><<<grid, threads, 0, s>>>(a); break;
+    case 128: few_keys_delta_kernel<T, 128><<<grid, threads, 0, s>>>(a); break;
+    default: return FA_ERR_ARG;
+  }
+  return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+}
+
 // Large blocks where they come to two per SM.
 template <typename T, int D>
 fa_status run(const Args& a, bool bwd, cudaStream_t s) {
@@ -663,6 +734,33 @@ fa_status launch_fwd_prefix_ffma(const FwdParams& p, cudaStream_t s) {
   copy4(a.sq, p.sq); copy4(a.sk, p.sk); copy4(a.sv, p.sv); copy4(a.so, p.so);
   a.causal = p.causal; a.scale = p.scale; a.status = p.status;
   return run_any(a, p.D, p.dtype, false, s);
+}
+
+// Small fp16 / bf16 gradients: the longest walk of a block (or of its share of a
+// cluster's), times the rounds of blocks, against the three launches of the tensor
+// cores' kernels (32 to 62 us).  A step takes 4, 6 and 11 us at D <= 32, 64 and 128.  4
+// sequences of 30 rows, 8 heads of 64, 10 prefix keys: 21 us here, 39 there; 3 of 130 rows,
+// 4 heads, 200 keys: 54 and 49.
+bool prefix_ffma_pays(const BwdParams& p) {
+  const Geo& g = p.g;
+  Args a{};
+  a.g = g; a.pfx = p.pfx;
+  const int D = static_cast<int>(p.D);
+  const int64_t blocks = bwd_blocks(a, 16), pre = p.pfx.P > 0 ? g.rows_q : 0;
+  const int64_t keys = tiles(p.pfx.P, BC) + tiles(g.Nk, BC);
+  const int64_t walk = g.G * tiles(pre > g.Nq ? pre : g.Nq, BC), cl = pick_cluster(blocks, keys, 4);
+  const int64_t steps = ((walk > keys ? walk : keys) + cl - 1) / cl;
+  const int64_t fit = 233472 / (bwd_smem(D, 16) + 1024), slots = device_sm_count() * (fit < 4 ? fit : 4);
+  return steps * ((blocks * cl + slots - 1) / slots) <= (D <= 32 ? 6 : 4);
+}
+
+fa_status launch_few_keys_delta(const BwdParams& p, float* delta, cudaStream_t s) {
+  Args a{};
+  a.q = p.q; a.k = p.k; a.v = p.v; a.dout = p.dout; a.lse_in = p.lse; a.delta_out = delta;
+  a.g = p.g; a.pfx = p.pfx;
+  copy4(a.sq, p.sq); copy4(a.sk, p.sk); copy4(a.sv, p.sv); copy4(a.sdo, p.sdo);
+  a.causal = p.causal; a.scale = p.scale; a.status = p.status;
+  return p.dtype == FA_F16 ? launch_few_keys<__half>(a, p.D, s) : launch_few_keys<__nv_bfloat16>(a, p.D, s);
 }
 
 fa_status launch_bwd_prefix_ffma(const BwdParams& p, cudaStream_t s) {

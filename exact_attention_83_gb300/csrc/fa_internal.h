@@ -291,6 +291,10 @@ fa_status launch_fwd_ffma(const FwdParams& p, cudaStream_t s);
 fa_status launch_bwd_ffma(const BwdParams& p, cudaStream_t s);
 fa_status launch_fwd_prefix_ffma(const FwdParams& p, cudaStream_t s);   // pfx.on
 fa_status launch_bwd_prefix_ffma(const BwdParams& p, cudaStream_t s);
+bool prefix_ffma_pays(const BwdParams& p);       // a small gradient in 16 bits
+// Delta of rows that see at most kFewKeys keys, from P and dP (fp16, bf16; P < kFewKeys)
+constexpr int64_t kFewKeys = 32;
+fa_status launch_few_keys_delta(const BwdParams& p, float* delta, cudaStream_t s);
 fa_status launch_preprocess(const PreParams& p, cudaStream_t s);
 fa_status launch_fwd_tc(const FwdParams& p, cudaStream_t s);
 fa_status launch_bwd_tc(const BwdParams& p, cudaStream_t s);

@@ -57,7 +57,7 @@ query sees the whole prefix and its own sequence's keys:
                           max_seqlen_q, max_seqlen_k, causal, scale, rotary)
                                     -> o with autograd, also for the prefix
   attention_prefix_fwd / attention_prefix_bwd: the same with outputs allocated
-  fwd_prefix / bwd_prefix           write the tensors given
+  fwd_prefix / bwd_prefix_delta / bwd_prefix    write the tensors given
 
 Serving (fa_decode): the newest tokens of a batch whose keys are a prefix that
 all requests share, followed by each request's own cache rows:
@@ -104,7 +104,7 @@ EXPORTED = ("fa_fwd", "fa_bwd_preprocess", "fa_bwd", "fa_get_device_status",
             "fa_bwd_fused_workspace_bytes", "fa_bwd_fused", "fa_dropout_mask_bytes",
             "fa_dropout_mask", "fa_test_set_l2_bytes", "fa_rotary_fwd",
             "fa_rotary_bwd_workspace_bytes", "fa_rotary_bwd", "fa_decode_workspace_bytes",
-            "fa_decode", "fa_fwd_prefix", "fa_bwd_prefix")
+            "fa_decode", "fa_fwd_prefix", "fa_bwd_prefix_delta", "fa_bwd_prefix")
 
 
 class Problem(ctypes.Structure):
@@ -203,6 +203,8 @@ def load_library(path: str = LIB_PATH):
         lib.fa_rotary_bwd.restype = ctypes.c_int
         lib.fa_fwd_prefix.argtypes = [_vp, _i64] + [_vp] * 14
         lib.fa_fwd_prefix.restype = ctypes.c_int
+        lib.fa_bwd_prefix_delta.argtypes = [_vp, _i64] + [_vp] * 17
+        lib.fa_bwd_prefix_delta.restype = ctypes.c_int
         lib.fa_bwd_prefix.argtypes = [_vp, _i64] + [_vp] * 25
         lib.fa_bwd_prefix.restype = ctypes.c_int
         lib.fa_decode_workspace_bytes.argtypes = [_vp]
@@ -1044,6 +1046,12 @@ def _fwd_prefix(pr, q, k, v, k_prefix, v_prefix, o, lse):
           *_addr(q, k_prefix, v_prefix, k, v, o), lse.data_ptr())
 
 
+def _bwd_prefix_delta(pr, q, k, v, k_prefix, v_prefix, o, do, lse, delta):
+    _call(load_library().fa_bwd_prefix_delta, "fa_bwd_prefix_delta", q.get_device(), pr,
+          k_prefix.shape[0], *_addr(q, k_prefix, v_prefix, k, v, o, do), lse.data_ptr(),
+          delta.data_ptr())
+
+
 def _bwd_prefix(pr, q, k, v, k_prefix, v_prefix, do, lse, delta, dq, dk, dv, dk_prefix, dv_prefix):
     _call(load_library().fa_bwd_prefix, "fa_bwd_prefix", q.get_device(), pr, k_prefix.shape[0],
           *_addr(q, k_prefix, v_prefix, k, v, do), lse.data_ptr(), delta.data_ptr(),
@@ -1061,11 +1069,22 @@ def fwd_prefix(q, k, v, k_prefix, v_prefix, o, lse, cu_seqlens_q, cu_seqlens_k, 
     _fwd_prefix(pr, q, k, v, k_prefix, v_prefix, o, lse)
 
 
+def bwd_prefix_delta(q, k, v, k_prefix, v_prefix, o, do, lse, delta, cu_seqlens_q, cu_seqlens_k,
+                     max_seqlen_q, max_seqlen_k, causal: bool = True, scale=None):
+    """fa_bwd_prefix_delta: delta [Hq, total_q] for bwd_prefix, without the rounding
+    of o in rows that see few keys."""
+    pr = _prefix_problem(q, k, v, k_prefix, v_prefix, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
+                         max_seqlen_k, causal, scale)
+    _like(q, o, do)
+    _lse_like(q, lse, delta)
+    _bwd_prefix_delta(pr, q, k, v, k_prefix, v_prefix, o, do, lse, delta)
+
+
 def bwd_prefix(q, k, v, k_prefix, v_prefix, do, lse, delta, dq, dk, dv, dk_prefix, dv_prefix,
                cu_seqlens_q, cu_seqlens_k, max_seqlen_q, max_seqlen_k, causal: bool = True,
                scale=None):
-    """fa_bwd_prefix: the gradients of fwd_prefix from its lse and delta =
-    rowsum(do * o), [Hq, total_q]."""
+    """fa_bwd_prefix: the gradients of fwd_prefix from its lse and bwd_prefix_delta's
+    delta = rowsum(do * o), [Hq, total_q]."""
     pr = _prefix_problem(q, k, v, k_prefix, v_prefix, cu_seqlens_q, cu_seqlens_k, max_seqlen_q,
                          max_seqlen_k, causal, scale)
     _like(q, do, dq)
@@ -1093,11 +1112,8 @@ def attention_prefix_bwd(q, k, v, k_prefix, v_prefix, o, lse, do, cu_seqlens_q, 
                          max_seqlen_k, causal, scale)
     _like(q, o, do)
     _lse_like(q, lse)
-    total, Hq, D = q.shape
     delta = torch.empty_like(lse)
-    _call(load_library().fa_bwd_preprocess, "fa_bwd_preprocess", q.get_device(), o.data_ptr(),
-          do.data_ptr(), delta.data_ptr(), 1, Hq, total, D, _strides4(o), _strides4(do),
-          _DTYPE_CODE[q.dtype])
+    _bwd_prefix_delta(pr, q, k, v, k_prefix, v_prefix, o, do, lse, delta)
     grads = [torch.empty_like(t, memory_format=torch.contiguous_format)
              for t in (q, k, v, k_prefix, v_prefix)]
     _bwd_prefix(pr, q, k, v, k_prefix, v_prefix, do, lse, delta, *grads)

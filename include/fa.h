@@ -344,7 +344,8 @@ FA_API fa_status fa_dropout_mask(const fa_problem* prob, uint8_t* mask, size_t b
  *   k_prefix, v_prefix, dk_prefix, dv_prefix   [1, Hkv, P, D] views, P >= 0
  *                                     (P = 0: ignored)
  *   lse, delta                        fp32 [Hq, total_q]; lse is over both sets of
- *                                     keys, delta = rowsum(dO o O) as for fa_bwd_ex
+ *                                     keys, delta = rowsum(dO o O) as for fa_bwd_ex,
+ *                                     from fa_bwd_prefix_delta
  * Strides and alignment as for fa_fwd, but no stride of 0 over an extent above
  * 1.  dk_prefix and dv_prefix sum over every sequence.  Results do not depend on
  * the schedule (no atomics).  Rows that belong to no sequence (before
@@ -354,6 +355,11 @@ FA_API fa_status fa_dropout_mask(const fa_problem* prob, uint8_t* mask, size_t b
  * behind it may be skipped too, and the gradients of the prefix are then not
  * defined.
  *
+ * fa_bwd_prefix_delta writes delta as fa_bwd_preprocess does, but for fp16 and
+ * bf16 rows that see at most 32 keys (with P < 32) as sum P dP, which is the same
+ * number without the rounding of O: with few keys that rounding shows in dq, dk
+ * and dk_prefix.  fa_bwd_preprocess's delta is taken too.
+ *
  * Errors as for fa_fwd_ex / fa_bwd_ex, plus FA_ERR_SHAPE for P < 0 or sequences
  * that are not packed, FA_ERR_ARG for dropout_p > 0.
  */
@@ -362,6 +368,13 @@ FA_API fa_status fa_fwd_prefix(const fa_problem* prob, int64_t P, const void* q,
                                const int64_t* svp, const void* k, const int64_t* sk, const void* v,
                                const int64_t* sv, void* o, const int64_t* so, float* lse,
                                cudaStream_t stream);
+FA_API fa_status fa_bwd_prefix_delta(const fa_problem* prob, int64_t P, const void* q,
+                                     const int64_t* sq, const void* k_prefix, const int64_t* skp,
+                                     const void* v_prefix, const int64_t* svp, const void* k,
+                                     const int64_t* sk, const void* v, const int64_t* sv,
+                                     const void* o, const int64_t* so, const void* dout,
+                                     const int64_t* sdo, const float* lse, float* delta,
+                                     cudaStream_t stream);
 FA_API fa_status fa_bwd_prefix(const fa_problem* prob, int64_t P, const void* q, const int64_t* sq,
                                const void* k_prefix, const int64_t* skp, const void* v_prefix,
                                const int64_t* svp, const void* k, const int64_t* sk, const void* v,

@@ -56,7 +56,7 @@ def make(lq, lk, Hq, Hkv, D, P, dtype="bf16", seed=0, lead=0, tail=0):
                 mq=max(max(lq), 1), mk=max(max(lk), 1))
 
 
-def reference(t, causal, scale=None):
+def reference(t, causal, scale=None, rounded_delta=True):
     """Values and magnitudes, {name: (value, bound without the final rounding)}."""
     Tq, Hq, D = t["q"].shape
     Tk, Hkv, _ = t["k"].shape
@@ -98,7 +98,7 @@ def reference(t, causal, scale=None):
             ddelta = (do.abs() * (bnd["o"][r, h] + u * o.abs())).sum(-1, keepdim=True)
             ds = p * (dp - delta)
             mds = p * (do.abs() @ vals.abs().T + (do * o).abs().sum(-1, keepdim=True))
-            eds = u * ds.abs() + SLACK * mds + p * ddelta
+            eds = u * ds.abs() + SLACK * mds + (p * ddelta if rounded_delta else 0.0)
             val["dq"][r, h] = ds @ keys * scale
             bnd["dq"][r, h] = eds @ keys.abs() * scale
             dk, ek = ds.T @ q * scale, eds.T @ q.abs() * scale
@@ -129,8 +129,8 @@ def run(t, causal, scale=None, train=True):
     return got
 
 
-def check(t, got, causal, scale=None):
-    val, bnd = reference(t, causal, scale)
+def check(t, got, causal, scale=None, rounded_delta=True):
+    val, bnd = reference(t, causal, scale, rounded_delta)
     dt = t["q"].dtype
     u = torch.finfo(dt).eps / 2
     rows = dict(q=slice(int(t["cq"][0]), int(t["cq"][-1])), k=slice(int(t["ck"][0]), int(t["ck"][-1])))
@@ -240,6 +240,60 @@ def test_bad_keys_of_an_empty_sequence_are_reported(D):
     torch.cuda.synchronize()
     assert fa.device_status() == 13 and fa.device_status() == 0
     assert torch.equal(got[:305], o[:305])
+
+
+@pytest.mark.parametrize("P", [0, 1, 3, 31, 32, 63, 65, 129])
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("fp16", 64), ("bf16", 32)])
+def test_short_prefixes_of_many_sequences(P, dtype, D):
+    """Too much for the FFMA kernels to pay: the tensor-core kernels at prefixes
+    of up to two tiles."""
+    lens = [(i * 41) % 150 for i in range(24)]
+    t = make(lens, lens, 8, 4, D, P, dtype, seed=21, lead=3, tail=5)
+    both(t)
+    both(t, False)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dtype,D", [("bf16", 128), ("fp16", 64), ("bf16", 32), ("fp16", 16)])
+@pytest.mark.parametrize("n,P", [(1, 1), (3, 11), (40, 11), (40, 0), (30, 2)])
+def test_gradients_of_rows_with_few_keys(n, P, dtype, D, causal):
+    """At most 32 keys per row: Delta comes without the rounding of o, so the
+    gradients' bound has no term for it; few rows (FFMA) and many (tensor cores)."""
+    lens = [1 + (7 * i + n) % 20 for i in range(n)] if n > 1 else [1]
+    t = make(lens, lens, 8, 4, D, P, dtype, seed=22, lead=2, tail=1)
+    args = (t["cq"], t["ck"], t["mq"], t["mk"], causal)
+    o, lse = fa.attention_prefix_fwd(t["q"], t["k"], t["v"], t["kp"], t["vp"], *args)
+    delta = torch.full_like(lse, 7.0)
+    fa.bwd_prefix_delta(t["q"], t["k"], t["v"], t["kp"], t["vp"], o, t["do"], lse, delta, *args)
+    grads = [torch.full_like(t[x], 7.0) for x in ("q", "k", "v", "kp", "vp")]
+    ts = (t["q"], t["k"], t["v"], t["kp"], t["vp"])
+    fa.bwd_prefix(*ts, t["do"], lse, delta, grads[0], grads[1], grads[2], grads[3], grads[4], *args)
+    torch.cuda.synchronize()
+    assert fa.device_status() == 0
+    check(t, dict(zip(("dq", "dk", "dv", "dkp", "dvp"), grads)), causal, rounded_delta=False)
+
+
+def test_few_keys_of_unequal_sequences_keep_rowsum_elsewhere():
+    """Rows above 32 keys take fa_bwd_preprocess's delta, bit for bit."""
+    lens = [100, 5, 0, 33, 20]
+    t = make(lens, lens, 4, 2, 64, 12, "bf16", seed=23)
+    for causal in (True, False):
+        args = (t["cq"], t["ck"], t["mq"], t["mk"], causal)
+        o, lse = fa.attention_prefix_fwd(t["q"], t["k"], t["v"], t["kp"], t["vp"], *args)
+        plain, delta = torch.empty_like(lse), torch.empty_like(lse)
+        fa.bwd_preprocess(fa._as4(o, True), fa._as4(t["do"], True), plain)
+        fa.bwd_prefix_delta(t["q"], t["k"], t["v"], t["kp"], t["vp"], o, t["do"], lse, delta, *args)
+        few = torch.zeros(sum(lens), dtype=torch.bool, device=DEV)
+        at = 0
+        for n in lens:
+            keys = 12 + (torch.arange(n, device=DEV) + 1 if causal else torch.full((n,), n, device=DEV))
+            few[at:at + n] = keys <= 32
+            at += n
+        assert torch.equal(delta[:, ~few], plain[:, ~few])
+        assert 20 <= int(few.sum()) < 120
+        u = 2.0**-8
+        mag = (t["do"].float().abs() * o.float().abs()).sum(-1).T
+        assert ((delta - plain).abs() <= 4 * u * mag + 1e-2)[:, few].all()
 
 
 def test_scale_strides_and_slices():

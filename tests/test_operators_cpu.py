@@ -173,6 +173,16 @@ def test_prefix_validation(lib):
         return lib.fa_bwd_prefix(ctypes.byref(pr), P, FAKE, st, FAKE, st, FAKE, st, FAKE, st, FAKE, st, FAKE,
                                  st, FAKE, delta, dq, st, dkp, st, FAKE, st, FAKE, sdk, FAKE, st, None)
 
+    def delta(pr, P=70, q=FAKE, kp=FAKE, o=FAKE, so=st, lse=FAKE, out=FAKE):
+        return lib.fa_bwd_prefix_delta(ctypes.byref(pr) if pr is not None else None, P, q, st, kp, st, FAKE, st,
+                                       FAKE, st, FAKE, st, o, so, FAKE, st, lse, out, None)
+
+    assert delta(None) == 1
+    assert delta(_packed(D=96)) == 3 and delta(_packed(), P=-1) == 2
+    assert delta(_packed(), q=None) == 1 and delta(_packed(), kp=None) == 1
+    assert delta(_packed(), o=None) == 1 and delta(_packed(), lse=None) == 1 and delta(_packed(), out=None) == 1
+    assert delta(_packed(), out=FAKE + 4) == 6 and delta(_packed(), so=S4(0, 0, 256, 1)) == 5
+
     assert fwd(None) == 1
     for call in (fwd, bwd):
         for kw, code in ((dict(dtype=9), 4), (dict(Hkv=3), 2), (dict(D=48), 3), (dict(scale=0.0), 10),
