@@ -49,7 +49,11 @@
 // maximum and sum over both, so nothing is joined or rounded in between.  The
 // prefix's last tile is zero-filled by its tensor map; the rows of a
 // sequence's last own V tile that belong to the next sequence (or to padding)
-// are zeroed before the product.
+// are zeroed before the product.  At D = 128 the two query tiles of a CTA are the
+// same rows of two heads that share a key/value head, if the heads come in such
+// pairs: both walk the same keys, and a short sequence wastes the rest of one tile
+// instead of two (16 sequences of up to 512 rows, 32 / 8 heads, 4096 prefix keys:
+// 259 us, 308 with the tiles 2i and 2i + 1 of one head).
 //
 // Every mbarrier wait is bounded (see tc_common.cuh); a wait that runs out
 // records FA_ERR_TIMEOUT, the CTA drains its copies and MMAs in flight,
@@ -100,6 +104,7 @@ struct FwdTcArgs {
   uint64_t timeout_ns;
   int withhold_arrival;    // test-only: CTA 0 skips the first S-ready arrival of tile 0
   PackedOrder order;       // template flag PFX
+  int hpair;               // template flag PFX: a CTA's two tiles are of two heads
 };
 
 template <typename T, int D, int DROP, bool PFX>
@@ -130,24 +135,31 @@ __global__ void __launch_bounds__(320, 1)
   // Grouped order (grouped_tile): the CTAs in flight belong to a few heads,
   // whose K and V tiles stay in L2; the longest query-tile pairs first.
   int64_t bh, t, h, bseq, pr;                   // bh = b * Hq + h; query-tile pair
+  const bool hpair = PFX && a.hpair;            // pr is then one tile, h the first of two heads
+  const int64_t H = hpair ? a.g.Hq / 2 : a.g.Hq;
   if (PFX && a.order.on) {
-    if (!packed_tile(a.order, a.g.cu_q, a.g.B, a.g.Nq, 2 * C::BM, a.g.Hq, id, a.causal != 0, h, bseq, pr))
+    if (!packed_tile(a.order, a.g.cu_q, a.g.B, a.g.Nq, hpair ? C::BM : 2 * C::BM, H, id, a.causal != 0, h,
+                     bseq, pr))
       return;
-    bh = bseq * a.g.Hq + h;
+    bh = bseq * H + h;
   } else {
     grouped_tile(id, a.BH, a.npairs, a.hgroup, bh, t);
     pr = a.causal ? (a.npairs - 1 - t) : t;
-    h = bh % a.g.Hq;
-    bseq = bh / a.g.Hq;
+    h = bh % H;
+    bseq = bh / H;
   }
+  if (hpair) h *= 2;
+  // query tile and head of tile g
+  const auto qt_of = [&](int g) -> int64_t { return hpair ? pr : 2 * pr + g; };
+  const auto hq_of = [&](int g) { return static_cast<int32_t>(hpair ? h + g : h); };
   const SeqView sv = seq_view(a.g, bseq);
   if (!sv.ok) {
     if (threadIdx.x == 0) record_status(a.status, FA_ERR_SEQLENS);
     return;
   }
   const int64_t Nq = sv.nq, Nk = sv.nk;
-  if (2 * pr * C::BM >= Nq) return;             // both query tiles lie past this sequence
-  const int32_t hq = static_cast<int32_t>(h), hk = static_cast<int32_t>(h / a.g.G);
+  if (qt_of(0) * C::BM >= Nq) return;           // both query tiles lie past this sequence
+  const int32_t hk = static_cast<int32_t>(h / a.g.G);
   const int32_t bb = static_cast<int32_t>(sv.b);
   const int nk = static_cast<int>((Nk + C::BN - 1) / C::BN);
   int np = 0;                                   // prefix tiles, before the own ones
@@ -155,7 +167,7 @@ __global__ void __launch_bounds__(320, 1)
   int ntile[2];
 #pragma unroll
   for (int g = 0; g < 2; ++g) {
-    const int64_t qt = 2 * pr + g;
+    const int64_t qt = qt_of(g);
     const int64_t diag = qt + 1;   // key tiles up to and including the diagonal
     ntile[g] = (qt * C::BM >= Nq) ? 0 : np + (a.causal ? static_cast<int>(diag < nk ? diag : nk) : nk);
   }
@@ -163,11 +175,12 @@ __global__ void __launch_bounds__(320, 1)
   if (nmax == 0) {
     // No key at all (an empty key sequence): O = 0 and L = -inf.
     if (warp < 8) {
-      const int64_t qrow = (2 * pr + (warp >> 2)) * C::BM + (warp & 3) * 32 + lane;
+      const int64_t qrow = qt_of(warp >> 2) * C::BM + (warp & 3) * 32 + lane;
       if (qrow < Nq) {
+        const int32_t hq = hq_of(warp >> 2);
         T* orow = static_cast<T*>(a.o) + bb * a.so[0] + hq * a.so[1] + (sv.q0 + qrow) * a.so[2];
         for (int d = 0; d < a.dreal; ++d) orow[d] = Elem<T>::from_f32(0.f);
-        a.lse[lse_index(a.g, sv, h, qrow)] = -INFINITY;
+        a.lse[lse_index(a.g, sv, hq, qrow)] = -INFINITY;
       }
     }
     return;
@@ -233,7 +246,7 @@ __global__ void __launch_bounds__(320, 1)
         if (ntile[g] == 0) continue;
         for (int c = 0; c < C::DC; ++c)
           tma_load_4d(smem_u32(sQ + g * C::TILE + c * C::CHUNK), &tmq, b_q, c * 64,
-                      static_cast<int32_t>(sv.q0 + (2 * pr + g) * C::BM), hq, bb);
+                      static_cast<int32_t>(sv.q0 + qt_of(g) * C::BM), hq_of(g), bb);
       }
       for (int u = 0; u < u_early; ++u) issue_unit(u);
     }
@@ -350,7 +363,8 @@ __global__ void __launch_bounds__(320, 1)
     // ------------------------------------------------------------ softmax + epilogue
     const int g = warp >> 2, quarter = warp & 3;
     const int r = quarter * 32 + lane;                       // row in the query tile
-    const int64_t qt = 2 * pr + g;
+    const int64_t qt = qt_of(g);
+    const int32_t hq = hq_of(g);
     const int64_t qrow = qt * C::BM + r;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>(quarter * 32) << 16);
     const uint32_t tS = lane_base + C::COL_S0 + 128 * g;
@@ -365,7 +379,7 @@ __global__ void __launch_bounds__(320, 1)
     // per key tile, tiles rows_q entries apart) for the backward
     uint4* mrow = nullptr;
     if (DROP && a.drop.mask != nullptr && qrow < Nq)
-      mrow = reinterpret_cast<uint4*>(a.drop.mask + mask_entry(a.drop, a.g, sv, h, 0, qrow));
+      mrow = reinterpret_cast<uint4*>(a.drop.mask + mask_entry(a.drop, a.g, sv, hq, 0, qrow));
     for (int j = 0; j < n; ++j) {
       // Dropout keep bits of this row's 128 keys, drawn before the scores
       // arrive (positions only): bit k of kb[k / 32] is key j*128 + k.
@@ -511,7 +525,7 @@ __global__ void __launch_bounds__(320, 1)
         tc_fence_after();
         const float inv = (DROP ? a.drop.rscale : 1.f) / l;   // Z's 1 / (1 - p) with dropout
         stage_row_sw128<T>(tO, inv, stg, r, 0, D);
-        if (qrow < Nq) a.lse[lse_index(a.g, sv, h, qrow)] = (m + log2f(l)) * kLn2;
+        if (qrow < Nq) a.lse[lse_index(a.g, sv, hq, qrow)] = (m + log2f(l)) * kLn2;
       }
       if (bar_red_and(1 + g, 128, ok)) {
         T* row0 = static_cast<T*>(a.o) + bb * a.so[0] + hq * a.so[1] + (sv.q0 + qt * C::BM) * a.so[2];
@@ -991,8 +1005,15 @@ fa_status run_fwd_tc(const FwdParams& p, cudaStream_t stream) {
         mq, mk, mv, a, px);
   } else {
     if constexpr (PFX) {
-      a.order = packed_order(g, g.Hq, g.rows_q, 256, blocks, p.pfx.P, p.D);
-      if (a.order.on) blocks = g.Hq * a.order.bound;
+      a.hpair = g.G % 2 == 0;
+      const int64_t H = a.hpair ? g.Hq / 2 : g.Hq;
+      const int rows = a.hpair ? 128 : 256;
+      a.BH = g.B * H; a.npairs = (g.Nq + rows - 1) / rows;
+      a.hgroup = head_group(a.BH, 2 * (g.Nk + p.pfx.P) * p.D * 2);
+      blocks = a.BH * a.npairs;
+      if (blocks > 0x7fffffffLL) return FA_ERR_SHAPE;
+      a.order = packed_order(g, H, g.rows_q, rows, blocks, p.pfx.P, p.D);
+      if (a.order.on) blocks = H * a.order.bound;
     }
     auto kern = fwd_tc_kernel<T, D, DROP, PFX>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM) !=
