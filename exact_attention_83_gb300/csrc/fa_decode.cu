@@ -924,7 +924,6 @@ template <typename T>
 __global__ void __launch_bounds__(kOwnThreads) join_kernel(const __grid_constant__ OwnArgs a) {
   constexpr int PIECES = kMaxRanges + kMaxChunks;
   __shared__ float sW[kOwnWarps][PIECES];
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * kOwnWarps + warp;   // of Hkv * R
   if (row >= static_cast<int64_t>(a.Hkv) * a.R) return;
@@ -933,6 +932,7 @@ __global__ void __launch_bounds__(kOwnThreads) join_kernel(const __grid_constant
   const int len = __ldg(a.lens + b);
   if (len < 0 || len > a.S) return;          // reported by own_kernel
   const int nc = len / a.chunk + (len % a.chunk != 0), n = a.ns + nc;
+  asm volatile("griddepcontrol.wait;" ::: "memory");       // the sums of both kernels
   auto piece_l = [&](int i) {
     return i < a.ns ? a.part_l[(static_cast<int64_t>(hk) * a.ns + i) * a.R + r]
                     : a.own_l[(static_cast<int64_t>(hk) * a.chunks + i - a.ns) * a.R + r];
