@@ -781,7 +781,8 @@ fa_status fa_decode(const fa_decode_problem* prob, const void* q, const int64_t*
   }
   FA_TRY(check_dense(o, so, p.B, Hq, p.Nq, p.dtype, p.so));
   FA_TRY(check_f32_vec(lse));
-  const size_t need = fa_decode_workspace_bytes(prob);
+  p.plan = decode_plan(p.B, p.Hkv, p.G * p.Nq, p.D, p.P, p.S);
+  const size_t need = static_cast<size_t>(p.plan.floats) * sizeof(float);
   if (need > 0) {
     FA_TRY(check_f32_vec(workspace));
     if (workspace_bytes < need) return FA_ERR_SCRATCH;

@@ -1062,7 +1062,7 @@ int own_rows(int64_t GN) { return GN <= 8 ? 8 : 16; }
 template <typename T, int D>
 fa_status run_decode(const DecodeParams& p, cudaStream_t stream) {
   const int64_t GN = p.G * p.Nq, R = p.B * GN;
-  const DecodePlan pl = decode_plan(p.B, p.Hkv, GN, p.D, p.P, p.S);
+  const DecodePlan& pl = p.plan;
   float* part_o = p.ws;
   float* part_l = part_o + static_cast<int64_t>(pl.ns) * p.Hkv * R * p.D;
   // the log-sum-exps take whole 16-byte units, so that the sums behind them stay aligned

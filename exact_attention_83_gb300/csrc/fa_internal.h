@@ -255,6 +255,14 @@ struct RotaryParams {
 constexpr int kRotaryMaxParts = 304;
 fa_status launch_rotary(const RotaryParams& p, cudaStream_t s);
 
+// How fa_decode cuts its work: ns ranges of the prefix's key tiles (0: no
+// prefix) for row groups of 256 (two = 1) or 128 query rows, and chunks of
+// `chunk` own rows per request; apart: the own rows leave their sums for a join;
+// floats: the workspace that takes.
+struct DecodePlan {
+  int ns, two, chunks, apart;
+  int64_t groups, chunk, floats;
+};
 // Parameters of one fa_decode call.
 struct DecodeParams {
   const void* q; const void* kp; const void* vp; const void* k; const void* v;
@@ -265,17 +273,10 @@ struct DecodeParams {
   int causal;
   float scale;
   fa_dtype dtype;
+  DecodePlan plan;
   float* ws;
   unsigned int* status;
   uint64_t timeout_ns;
-};
-// How fa_decode cuts its work: ns ranges of the prefix's key tiles (0: no
-// prefix) for row groups of 256 (two = 1) or 128 query rows, and chunks of
-// `chunk` own rows per request; apart: the own rows leave their sums for a join;
-// floats: the workspace that takes.
-struct DecodePlan {
-  int ns, two, chunks, apart;
-  int64_t groups, chunk, floats;
 };
 DecodePlan decode_plan(int64_t B, int64_t Hkv, int64_t GN, int64_t D, int64_t P, int64_t S);
 fa_status launch_decode(const DecodeParams& p, cudaStream_t s);

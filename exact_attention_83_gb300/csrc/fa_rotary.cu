@@ -694,20 +694,36 @@ Tiles make_tiles(const RotaryParams& p, int tok) {
   return t;
 }
 
-// The tokens per tile with which `slots` blocks end first, walking tiles whose
-// heads cost `heads(tok)`.  Long tiles cost less in all, short ones spread short
-// inputs over the SMs and leave less of the last round idle.
+// The tiles to choose from, with what each costs a block whose heads cost
+// `heads(tok)`.
+struct TileOptions {
+  int n;
+  Tiles t[8];
+  double cost[8];
+};
 template <typename Cost>
-Tiles pick_tiles(const RotaryParams& p, int64_t slots, Cost heads, double* time) {
+TileOptions tile_options(const RotaryParams& p, Cost heads) {
+  TileOptions o{};
+  for (int tok = static_cast<int>(2048 / p.D); tok >= 1; tok /= 2, ++o.n) {
+    o.t[o.n] = make_tiles(p, tok);
+    o.cost[o.n] = heads(tok) + tile_cost(p, tok);
+  }
+  return o;
+}
+static_assert(kMostTokens == 1 << 7, "eight tile lengths");
+
+// The tiles with which `slots` blocks end first.  Long tiles cost less in all,
+// short ones spread short inputs over the SMs and leave less of the last round
+// idle.
+Tiles pick_tiles(const TileOptions& o, int64_t slots, double* time) {
   Tiles best{};
   *time = 0;
-  for (int tok = static_cast<int>(2048 / p.D); tok >= 1; tok /= 2) {
-    const Tiles t = make_tiles(p, tok);
-    const int64_t grid = t.items < slots ? t.items : slots;
-    const double ms = static_cast<double>((t.items + grid - 1) / grid) * (heads(tok) + tile_cost(p, tok));
+  for (int i = 0; i < o.n; ++i) {
+    const int64_t rounds = o.t[i].items <= slots ? 1 : (o.t[i].items + slots - 1) / slots;
+    const double ms = static_cast<double>(rounds) * o.cost[i];
     if (*time == 0 || ms < *time) {
       *time = ms;
-      best = t;
+      best = o.t[i];
     }
   }
   return best;
@@ -737,8 +753,8 @@ fa_status run_fwd(const RotaryParams& p, cudaStream_t s) {
   const int64_t slots = static_cast<int64_t>(device_sm_count()) * fwd_blocks<T>(NORM);
   RotArgs a = make_args(p);
   double time;
-  a.tiles[0] = pick_tiles(p, slots, [&](int tok) { return head_cost(p.Hq, D, tok) + head_cost(p.Hkv, D, tok); },
-                          &time);
+  const auto heads = [&](int tok) { return head_cost(p.Hq, D, tok) + head_cost(p.Hkv, D, tok); };
+  a.tiles[0] = pick_tiles(tile_options(p, heads), slots, &time);
   a.sign = p.backward ? -1.f : 1.f;      // without a norm the gradient is the rotation back
   const int64_t grid = a.tiles[0].items < slots ? a.tiles[0].items : slots;
   FA_CONFIGURE((rotary_kernel<T, D, NORM, IL>), kFwdSmem<T>);
@@ -758,11 +774,12 @@ fa_status run_bwd(const RotaryParams& p, cudaStream_t s) {
   const int ref = static_cast<int>(1024 / D);
   const double cq = head_cost(p.Hq, D, ref) + tile_cost(p, ref), ck = head_cost(p.Hkv, D, ref) + tile_cost(p, ref);
   const int64_t mid = static_cast<int64_t>(static_cast<double>(slots) * cq / (cq + ck));
+  const TileOptions oq = tile_options(p, [&](int tok) { return head_cost(p.Hq, D, tok); });
+  const TileOptions ok = tile_options(p, [&](int tok) { return head_cost(p.Hkv, D, tok); });
   for (int64_t q = mid - 16; q <= mid + 16; q += 4) {
     if (q < 1 || q >= slots) continue;
     double tq, tk;
-    const Tiles lq = pick_tiles(p, q, [&](int tok) { return head_cost(p.Hq, D, tok); }, &tq);
-    const Tiles lk = pick_tiles(p, slots - q, [&](int tok) { return head_cost(p.Hkv, D, tok); }, &tk);
+    const Tiles lq = pick_tiles(oq, q, &tq), lk = pick_tiles(ok, slots - q, &tk);
     const double t = tq > tk ? tq : tk;
     if (best == 0 || t < best) {
       best = t;
