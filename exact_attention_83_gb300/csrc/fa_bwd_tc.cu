@@ -1770,6 +1770,27 @@ fa_status run_bwd_tc(const BwdParams& p, cudaStream_t stream) {
   return FA_OK;
 }
 
+// CTAs (one cluster) that share a key tile's walk of `steps` query tiles.  Larger
+// clusters shorten the walk, but each costs its join (12 us), and of 152 SMs, one CTA
+// each, clusters of 1, 2, 4 and 8 fill 152, 152, 112 and 64.  16 sequences of up to 512
+// rows, D = 128, us for 1 / 2 / 4 / 8: 8 key/value heads of 4, 4096 prefix keys 400 / 449 /
+// 601 / -, 2048 keys 202 / 226 / 302 / -; 2 of 8, 4096 keys 389 / 209 / 247 / 490; 1 of 8,
+// 2000 keys 386 / 207 / 123 / 195.
+int pick_split(int64_t walks, int64_t G, int64_t steps, double step_us) {
+  constexpr int kAtOnce[4] = {152, 76, 28, 8};
+  int best = 1;
+  double least = 0;
+  for (int i = 0; i < 4 && G % (1 << i) == 0; ++i) {
+    const double t = static_cast<double>((walks + kAtOnce[i] - 1) / kAtOnce[i]) *
+                     (static_cast<double>(steps) * step_us / (1 << i) + (i ? 12.0 : 2.0));
+    if (i == 0 || t < least) {
+      least = t;
+      best = 1 << i;
+    }
+  }
+  return best;
+}
+
 // dK / dV of one set of keys (`g`: the sequences' own, or the prefix against
 // all query rows) for the prefix entry points.
 template <typename T, int D>
@@ -1780,12 +1801,12 @@ fa_status launch_dkdv_zr(const BwdParams& p, const Geo& g, const CUtensorMap& mq
   a.BH = g.B * g.Hkv; a.ntiles = (g.Nk + 127) / 128;
   a.hgroup = head_group(a.BH, 2 * g.Nq * p.D * 2 * g.G);
   const int64_t base = a.BH * a.ntiles;
-  int split = 1;
-  while (split < 8 && g.G % (2 * split) == 0 && base * split < 2 * device_sm_count()) split *= 2;
-  a.split = split;
-  if (base * split > 0x7fffffffLL) return FA_ERR_SHAPE;
+  if (base > 0x7fffffffLL / 8) return FA_ERR_SHAPE;
   a.order = g.cu_k ? packed_order(g, g.Hkv, g.rows_k, 128, base, 0, p.D) : PackedOrder{};
-  const int64_t blocks = (a.order.on ? g.Hkv * a.order.bound : base) * split;
+  const int64_t walks = a.order.on ? g.Hkv * a.order.bound : base;
+  const int split = pick_split(walks, g.G, g.G * ((g.Nq + 127) / 128), D > 64 ? 1.39 : 1.22);
+  a.split = split;
+  const int64_t blocks = walks * split;
   auto kern = bwd_dkdv_tc_kernel<T, D, kDropNone, true>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, DkdvCfg<D>::SMEM) !=
       cudaSuccess)
