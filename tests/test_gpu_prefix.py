@@ -253,6 +253,17 @@ def test_short_prefixes_of_many_sequences(P, dtype, D):
     both(t, False)
 
 
+@pytest.mark.parametrize("Hq,Hkv", [(8, 1), (4, 1), (6, 1), (16, 2), (7, 1)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_walks_shared_by_clusters(Hq, Hkv, D):
+    """Few key tiles and many query rows: clusters of up to eight, for the own and
+    the prefix's keys."""
+    lens = (300, 1, 403, 130, 77, 260)
+    t = make(lens, lens, Hq, Hkv, D, 450, "bf16", seed=24, lead=1, tail=2)
+    both(t)
+    both(t, False)
+
+
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("dtype,D", [("bf16", 128), ("fp16", 64), ("bf16", 32), ("fp16", 16)])
 @pytest.mark.parametrize("n,P", [(1, 1), (3, 11), (40, 11), (40, 0), (30, 2)])
